@@ -10,6 +10,7 @@ this module raises.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -25,7 +26,9 @@ EXPORTS = ("mimi_rvq_create", "mimi_rvq_destroy", "mimi_rvq_encode", "mimi_rvq_e
            "mimi_rvq_encode_profile", "mimi_rvq_delay_pack", "mimi_rvq_delay_unpack",
            "mimi_rvq_embed_sum", "mimi_rvq_wait_selftest", "mimi_rvq_encode_step_ex",
            "mimi_rvq_encode_noalloc", "mimi_rvq_streams_get_error",
-           "mimi_rvq_streams_wait_selftest")
+           "mimi_rvq_streams_wait_selftest", "mimi_rvq_token_logprob",
+           "mimi_rvq_token_logprob_grad", "mimi_rvq_distill_topk", "mimi_rvq_distill_topk_grad")
+MAX_TOP, MAX_VOCAB = 128, 1 << 20
 TEXT_CARD, TEXT_PAD, AUDIO_PAD = 32000, 32000, 2048
 
 _lib = None
@@ -89,6 +92,17 @@ def library() -> ctypes.CDLL:
     lib.mimi_rvq_streams_get_error.restype = ci
     lib.mimi_rvq_streams_wait_selftest.argtypes = [vp]
     lib.mimi_rvq_streams_wait_selftest.restype = ci
+    rows = [vp, ci, i64, ci, ci, i64, i64]  # logits, dtype, S, n, V, strides
+    toks = [vp, i64, i64, i32, ctypes.c_float]  # tokens, strides, pad, scale
+    lib.mimi_rvq_token_logprob.argtypes = rows + toks + [ci] + [vp] * 7
+    lib.mimi_rvq_token_logprob.restype = ci
+    lib.mimi_rvq_token_logprob_grad.argtypes = rows + toks + [vp] * 4 + [i64] * 2 + [vp] * 5
+    lib.mimi_rvq_token_logprob_grad.restype = ci
+    teacher = [vp, vp, ci, ci, ci, ctypes.c_float]  # ids, teacher, dtype, k, tail, scale
+    lib.mimi_rvq_distill_topk.argtypes = rows + teacher + [vp] * 3
+    lib.mimi_rvq_distill_topk.restype = ci
+    lib.mimi_rvq_distill_topk_grad.argtypes = rows + teacher + [vp] * 2 + [i64] * 2 + [vp] * 3
+    lib.mimi_rvq_distill_topk_grad.restype = ci
     _lib = lib
     return lib
 
@@ -349,3 +363,187 @@ def streams_wait_selftest(stream=None):
     times out after ~50 ms; the next streams_get_error() returns -6."""
     _check(library().mimi_rvq_streams_wait_selftest(_stream(stream)),
            "mimi_rvq_streams_wait_selftest")
+
+
+# ----------------------------------------------------------------- logits over the streams
+
+TokenLogprobs = collections.namedtuple("TokenLogprobs",
+                                       "logprob entropy lse top_ids top_logprob")
+TokenLogprobs.__doc__ = """Values of token_logprobs: logprob, entropy, lse [S(, n)] float32,
+top_ids [S(, n), k] int32 and top_logprob [S(, n), k] float32; None where not wanted."""
+
+
+class _on:
+    """Run a call on `device` and `stream` (None: the device's current stream), so that its
+    outputs are allocated there too."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _logit_rows(logits):
+    """(lead shape, dtype flag, S, n, V, stride_s, stride_n) of [S, V] or [S, n, V] logits."""
+    assert logits.is_cuda and logits.dim() in (2, 3), "logits are [S, V] or [S, n, V] on CUDA"
+    shape, stride = logits.shape, logits.stride()
+    assert shape[-1] <= 1 or stride[-1] == 1, "a row's logits are contiguous"
+    if logits.dim() == 2:
+        return shape[:1], _dtype_flag(logits), shape[0], 1, shape[1], stride[0], 0
+    return shape[:2], _dtype_flag(logits), shape[0], shape[1], shape[2], stride[0], stride[1]
+
+
+def _row_tokens(tokens, lead, device):
+    """(pointer, stride_s, stride_n) of tokens of the rows' shape, any strides."""
+    import torch
+    if tokens is None:
+        return None, 0, 0
+    assert tokens.dtype == torch.int32 and tokens.shape == lead and tokens.device == device
+    st = tokens.stride()
+    return tokens.data_ptr(), st[0], st[1] if len(st) == 2 else 0
+
+
+def _row_array(t, shape, dtype, device):
+    """Pointer of a contiguous array of that shape, None for None."""
+    if t is None:
+        return None
+    assert t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device
+    return t.data_ptr()
+
+
+def _bad_counter(n_bad, device):
+    import torch
+    if n_bad is None:
+        return None
+    assert n_bad.dtype == torch.int64 and n_bad.numel() >= 1 and n_bad.device == device
+    return n_bad.data_ptr()
+
+
+def _gradient(out, logits):
+    """The gradient's tensor and its (stride_s, stride_n)."""
+    import torch
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    assert out.shape == logits.shape and out.dtype == logits.dtype and out.device == logits.device
+    st = out.stride()
+    assert out.shape[-1] <= 1 or st[-1] == 1
+    return out, (st[0], st[1] if out.dim() == 3 else 0)
+
+
+def token_logprobs(logits, tokens=None, pad=-1, scale=1.0, top_k=0, out=None, n_bad=None,
+                   stream=None):
+    """Log probabilities of the streams' tokens: logits [S, V] or [S, n, V] float32 / bfloat16
+    (CUDA, rows contiguous, any strides between rows), tokens [S] or [S, n] int32 (a view such
+    as packed[:, 1:9] is read in place; below 0 or equal to pad: no target, logprob 0).
+    Returns TokenLogprobs; logprob is None without tokens, the top lists are None for
+    top_k = 0. scale is 1 / temperature. out: TokenLogprobs of tensors to write, None in the
+    place of values that are not wanted. n_bad: optional CUDA int64 [1] (caller-zeroed)
+    counting tokens past V."""
+    import torch
+    lead, dt, S, n, V, ss, sn = _logit_rows(logits)
+    dev, f32 = logits.device, torch.float32
+    with _on(dev, stream):
+        if out is None:
+            e = torch.empty
+            out = TokenLogprobs(e(lead, dtype=f32, device=dev) if tokens is not None else None,
+                                e(lead, dtype=f32, device=dev), e(lead, dtype=f32, device=dev),
+                                e((*lead, top_k), dtype=torch.int32, device=dev) if top_k else None,
+                                e((*lead, top_k), dtype=f32, device=dev) if top_k else None)
+        top = (*lead, top_k)
+        _check(library().mimi_rvq_token_logprob(
+            logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, lead, dev), int(pad),
+            float(scale), int(top_k), _row_array(out.logprob, lead, f32, dev),
+            _row_array(out.entropy, lead, f32, dev), _row_array(out.lse, lead, f32, dev),
+            _row_array(out.top_ids, top, torch.int32, dev),
+            _row_array(out.top_logprob, top, f32, dev), _bad_counter(n_bad, dev),
+            _stream(stream)), "mimi_rvq_token_logprob")
+    return out
+
+
+def token_logprobs_grad(logits, tokens=None, g_logprob=None, g_entropy=None, g_lse=None, pad=-1,
+                        scale=1.0, values=None, out=None, n_bad=None, stream=None):
+    """Gradient of sum(g_logprob * logprob + g_entropy * entropy + g_lse * lse) with respect to
+    the logits, in the logits' type: g_* are [S] or [S, n] float32, None where there is none.
+    out may be the logits themselves. values = True, or a TokenLogprobs of tensors (top lists
+    None), also gives logprob, entropy and lse from the same pass: the call then returns
+    (dlogits, TokenLogprobs). Otherwise it returns dlogits."""
+    import torch
+    lead, dt, S, n, V, ss, sn = _logit_rows(logits)
+    dev, f32 = logits.device, torch.float32
+    with _on(dev, stream):
+        out, d_strides = _gradient(out, logits)
+        v = TokenLogprobs(None, None, None, None, None) if not values else values
+        if values is True:
+            e = torch.empty
+            v = TokenLogprobs(e(lead, dtype=f32, device=dev) if tokens is not None else None,
+                              e(lead, dtype=f32, device=dev), e(lead, dtype=f32, device=dev),
+                              None, None)
+        assert v.top_ids is None and v.top_logprob is None, "the gradient call lists no tokens"
+        _check(library().mimi_rvq_token_logprob_grad(
+            logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, lead, dev), int(pad),
+            float(scale), _row_array(g_logprob, lead, f32, dev),
+            _row_array(g_entropy, lead, f32, dev), _row_array(g_lse, lead, f32, dev),
+            out.data_ptr(), *d_strides, _row_array(v.logprob, lead, f32, dev),
+            _row_array(v.entropy, lead, f32, dev), _row_array(v.lse, lead, f32, dev),
+            _bad_counter(n_bad, dev), _stream(stream)), "mimi_rvq_token_logprob_grad")
+    return (out, v) if values else out
+
+
+def _teacher_list(ids, teacher, lead, device):
+    """(ids, teacher, teacher dtype, k) of a teacher's lists [S(, n), k]."""
+    import torch
+    assert ids.dim() == len(lead) + 1 and teacher.dtype in (torch.float32, torch.bfloat16)
+    shape = (*lead, ids.shape[-1])
+    return (_row_array(ids, shape, torch.int32, device),
+            _row_array(teacher, shape, teacher.dtype, device), _dtype_flag(teacher), shape[-1])
+
+
+def distill_topk(logits, ids, teacher, tail=False, scale=1.0, out=None, n_bad=None, stream=None):
+    """Loss [S] or [S, n] float32 of a student's logits against a teacher's top lists: ids
+    [S(, n), k] int32 (below 0: empty) and teacher [S(, n), k] float32 / bfloat16 as
+    token_logprobs(..., top_k=k) gives them. tail = False: KL to the list's softmax; tail =
+    True: the teacher's log probabilities as they are, with all other tokens as one more
+    class. scale applies to the student only."""
+    import torch
+    lead, dt, S, n, V, ss, sn = _logit_rows(logits)
+    dev = logits.device
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(lead, dtype=torch.float32, device=dev)
+        _check(library().mimi_rvq_distill_topk(
+            logits.data_ptr(), dt, S, n, V, ss, sn, *_teacher_list(ids, teacher, lead, dev),
+            1 if tail else 0, float(scale), _row_array(out, lead, torch.float32, dev),
+            _bad_counter(n_bad, dev), _stream(stream)), "mimi_rvq_distill_topk")
+    return out
+
+
+def distill_topk_grad(logits, ids, teacher, g=None, tail=False, scale=1.0, loss=None, out=None,
+                      n_bad=None, stream=None):
+    """Gradient of sum(g * loss) with respect to the logits, in their type (g [S] or [S, n]
+    float32, None: all 1; out may be the logits themselves). loss = True, or a float32 tensor
+    [S] or [S, n], also gives the losses from the same pass: the call then returns
+    (dlogits, loss). Otherwise it returns dlogits."""
+    import torch
+    lead, dt, S, n, V, ss, sn = _logit_rows(logits)
+    dev, f32 = logits.device, torch.float32
+    with _on(dev, stream):
+        out, d_strides = _gradient(out, logits)
+        if loss is True:
+            loss = torch.empty(lead, dtype=f32, device=dev)
+        _check(library().mimi_rvq_distill_topk_grad(
+            logits.data_ptr(), dt, S, n, V, ss, sn, *_teacher_list(ids, teacher, lead, dev),
+            1 if tail else 0, float(scale), _row_array(g, lead, f32, dev), out.data_ptr(),
+            *d_strides, _row_array(loss, lead, f32, dev), _bad_counter(n_bad, dev),
+            _stream(stream)), "mimi_rvq_distill_topk_grad")
+    return out if loss is None else (out, loss)
