@@ -1,0 +1,514 @@
+// logits.cuh -- what the kernels on the language model's logits share: a row's
+// layout, its loads, the pass that gives its softmax statistics, and the host
+// side's choice of threads.
+//
+// A row is one position of one stream: V logits that start at any element. It
+// is cut into 16-byte vectors on aligned addresses (the first and the last may
+// be partly outside the row: their outside elements read as -inf and are never
+// stored), and thread t of the TH that share a row takes vectors t, t + TH, ...
+// Up to NV vectors per thread are kept in registers, so a gradient reads its
+// row once; a longer part is walked in chunks of TH * NV vectors.
+//
+// Every statistic comes from m = max x, s = sum e^{c (x - m)} and
+// w = sum e^{c (x - m)} (x - m), c = scale, all in float32:
+//     lse = c m + ln s,  ln p_i = c (x_i - m) - ln s,  entropy = ln s - c w / s.
+// Each warp sums against its own maximum (one hardware reduction), so a row
+// needs one barrier, where the warps' triples are joined; a row split over a
+// cluster needs one cluster barrier more.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/mimi_rvq.h"
+#include "../../include/mimi_rvq_streams.h"
+#include "ptx.cuh"
+
+namespace mimi {
+namespace logits {
+
+constexpr int kMaxTop = MIMI_RVQ_MAX_TOP;
+constexpr int kMaxCluster = 8;  // CTAs that may share a row (the portable cluster size)
+constexpr float kInf = INFINITY;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kFull = 0xffffffffu;
+
+// The rows of a logits tensor [S][n][V]; strides in elements.
+struct RowsIn {
+    const void* x;
+    int64_t ss, sn;
+    int64_t rows;  // S * n
+    int n, V;
+    float c;       // scale
+    int cluster;   // CTAs per row (1: a row is one CTA's or one warp's)
+};
+
+// ------------------------------------------------------------------ elements
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+    static constexpr int kPer = 4;  // elements of a 16-byte vector
+    static constexpr uint32_t kFill = 0xFF800000u;
+};
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr int kPer = 8;
+    static constexpr uint32_t kFill = 0xFF80FF80u;
+};
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void narrow(float v, float* p) { *p = v; }
+__device__ __forceinline__ void narrow(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
+
+// element j of a vector
+template <typename T>
+__device__ __forceinline__ float element(const uint32_t (&w)[4], int j) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    else return __uint_as_float((j & 1) ? (w[j / 2] & 0xFFFF0000u) : (w[j / 2] << 16));
+}
+
+// a vector's elements plus `a` (one rounding each; bf16 widens exactly)
+__device__ __forceinline__ void add_to(const uint32_t (&w)[4], float a, float (&d)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = __uint_as_float(w[j]) + a;
+}
+__device__ __forceinline__ void add_to(const uint32_t (&w)[4], float a, float (&d)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %2;\n\t"
+            "add.rn.f32.bf16 %0, lo, %3;\n\t"
+            "add.rn.f32.bf16 %1, hi, %3;\n\t}"
+            : "=f"(d[2 * j]), "=f"(d[2 * j + 1])
+            : "r"(w[j]), "f"(a));
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "r"(kFull));
+    return r;
+}
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// A difference x - max below this has probability 0 in float32 (e^-200); clamping it there keeps
+// 0 times -inf out of the products with a probability.
+__device__ __forceinline__ float far_below(float c) { return fmaxf(-200.f / c, -3.0e38f); }
+
+// ln p of a logit of the row; the difference and product in float64, so that logits of opposite
+// sign near float32's limits do not overflow (a few of these per row).
+__device__ __forceinline__ float log_prob(float x, float c, float m, float ln_s) {
+    return (float)((double)c * ((double)x - (double)m) - (double)ln_s);
+}
+
+// ------------------------------------------------------------------ rows
+
+// One thread group's share of a row: vectors [v0, v1), of which [lo, hi) lie wholly in the row.
+template <typename T>
+struct Part {
+    const T* x;
+    int V;
+    int a;  // elements between the 16-byte boundary at or below x and x
+    int v0, v1, lo, hi;
+
+    static constexpr int kPer = Elem<T>::kPer;
+
+    __device__ Part(const T* row, int V_, int rank, int cluster) : x(row), V(V_) {
+        a = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+        const int all = (a + V + kPer - 1) / kPer;
+        const int per = (all + cluster - 1) / cluster;
+        v0 = min(rank * per, all);
+        v1 = min(v0 + per, all);
+        lo = max(v0, a ? 1 : 0);
+        hi = min(v1, (a + V) / kPer);
+    }
+    __device__ int size() const { return v1 - v0; }
+    // element index of a vector's first element (below 0 or past V at the row's ends)
+    __device__ int first(int vec) const { return vec * kPer - a; }
+    // vector and place of an element
+    __device__ int vector_of(int i) const { return (i + a) / kPer; }
+    __device__ bool holds(int vec) const { return vec >= v0 && vec < v1; }
+};
+
+__device__ __forceinline__ void load16(const void* p, uint32_t (&w)[4]) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store16(void* p, const uint32_t (&w)[4]) {
+    asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+
+// The vector at a row's end, element by element; -inf outside the row.
+template <typename T>
+__device__ __noinline__ uint4 load_edge(const T* x, int first, int V) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = Elem<T>::kFill;
+#pragma unroll
+    for (int j = 0; j < Elem<T>::kPer; ++j) {
+        const int i = first + j;
+        if (i >= 0 && i < V) {
+            if constexpr (sizeof(T) == 4) {
+                w[j] = __float_as_uint(x[i]);
+            } else {
+                const uint32_t b = __bfloat16_as_ushort(x[i]);
+                w[j / 2] = (j & 1) ? ((w[j / 2] & 0xFFFFu) | (b << 16)) : ((w[j / 2] & 0xFFFF0000u) | b);
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A vector's gradients, rounded once: whole at an aligned place, or element by element (those of
+// the row) where the row's ends or the gradient's own alignment want it.
+template <typename T>
+__device__ __forceinline__ void store_vector(T* row, int first, const float (&y)[4], bool whole,
+                                             bool some, int V) {
+    if (whole) {
+        const uint32_t w[4] = {__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                               __float_as_uint(y[3])};
+        store16(row + first, w);
+    } else if (some) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (first + j >= 0 && first + j < V) narrow(y[j], row + first + j);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_vector(T* row, int first, const float (&y)[8], bool whole,
+                                             bool some, int V) {
+    if (whole) {
+        const uint32_t w[4] = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                               pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
+        store16(row + first, w);
+    } else if (some) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (first + j >= 0 && first + j < V) narrow(y[j], row + first + j);
+    }
+}
+
+// Loads vector `vec` of the row's ends into its place of the chunk, if it is this thread's.
+template <int TH, int NV, typename T>
+__device__ __forceinline__ void put_edge(const Part<T>& p, int vec, int base, int tid,
+                                         uint32_t (&v)[NV][4]) {
+    const int at = vec - base - tid;
+    if (vec < p.v0 || vec >= p.v1 || at < 0 || at >= NV * TH || at % TH != 0) return;
+    const uint4 w = load_edge(p.x, p.first(vec), p.V);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const bool here = at == i * TH;
+        v[i][0] = here ? w.x : v[i][0];
+        v[i][1] = here ? w.y : v[i][1];
+        v[i][2] = here ? w.z : v[i][2];
+        v[i][3] = here ? w.w : v[i][3];
+    }
+}
+
+// A chunk's vectors: base + i * TH + tid, i < NV; -inf past the part's end.
+template <int TH, int NV, typename T>
+__device__ __forceinline__ void load_chunk(const Part<T>& p, int base, int tid,
+                                           uint32_t (&v)[NV][4]) {
+    const T* at = p.x + p.first(base + tid);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int vec = base + i * TH + tid;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = Elem<T>::kFill;
+        if (vec >= p.lo && vec < p.hi) load16(at + i * TH * Elem<T>::kPer, v[i]);
+    }
+    // the row's ends, where they are not whole vectors (one of them if the row is that short)
+    put_edge<TH, NV>(p, p.lo - 1, base, tid, v);
+    if (p.hi >= p.lo) put_edge<TH, NV>(p, p.hi, base, tid, v);
+}
+
+// Puts -inf in the place of marked elements: mark[i] has a bit per element of vector i.
+template <int NV, typename T>
+__device__ __forceinline__ void hide(const uint8_t* mark, uint32_t (&v)[NV][4]) {
+#pragma unroll
+    for (int h = 0; h < NV / 4; ++h) {
+        const uint32_t four = *reinterpret_cast<const uint32_t*>(mark + 4 * h);
+        if (four == 0) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t b = (four >> (8 * i)) & 0xFFu;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t& w = v[4 * h + i][j];
+                if constexpr (sizeof(T) == 4) {
+                    if ((b >> j) & 1u) w = Elem<T>::kFill;
+                } else {
+                    if ((b >> (2 * j)) & 1u) w = (w & 0xFFFF0000u) | 0xFF80u;
+                    if ((b >> (2 * j)) & 2u) w = (w & 0xFFFFu) | 0xFF800000u;
+                }
+            }
+        }
+    }
+}
+
+// f(vector of the chunk, its registers) for this thread's vectors below `here`, the number of
+// vectors from the chunk's base to the part's end; whole warps past it skip.
+template <int TH, int NV, typename F>
+__device__ __forceinline__ void each_vector(uint32_t (&v)[NV][4], int here, int tid, F&& f) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (i * TH + (tid & ~31) < here) f(i, v[i]);
+}
+
+struct Stats {
+    float m, s, w;  // m is -inf where no logit is finite
+};
+
+// Adds a chunk to a warp's running statistics: m is the warp's, s and w are the thread's.
+// top: the thread's own maximum over all chunks.
+template <int TH, int NV, bool kW, typename T>
+__device__ __forceinline__ void add_chunk(uint32_t (&v)[NV][4], int here, int tid, float c2,
+                                          float low, Stats& st, float& top) {
+    float mx;
+    if constexpr (sizeof(T) == 4) {
+        mx = -kInf;
+        each_vector<TH, NV>(v, here, tid, [&](int, uint32_t (&w)[4]) {
+            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]))),
+                       fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+        });
+    } else {
+        uint32_t a = Elem<T>::kFill;
+        each_vector<TH, NV>(v, here, tid, [&](int, uint32_t (&w)[4]) {
+            a = max_bf16x2(max_bf16x2(a, max_bf16x2(w[0], w[1])), max_bf16x2(w[2], w[3]));
+        });
+        mx = fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a));
+    }
+    top = fmaxf(top, mx);
+    const float m = fmaxf(st.m, warp_max(mx));
+    const float mu = m == -kInf ? 0.f : m;
+    if (st.m != m && st.m != -kInf) {  // an earlier chunk's sums move to the new maximum
+        const float d = st.m - m, f = ex2(d * c2);
+        if constexpr (kW) st.w = f * (st.w + st.s * fmaxf(d, low));
+        st.s *= f;
+    }
+    st.m = m;
+    float s0 = 0.f, s1 = 0.f, w0 = 0.f, w1 = 0.f;
+    each_vector<TH, NV>(v, here, tid, [&](int, uint32_t (&w)[4]) {
+        float d[Elem<T>::kPer];
+        add_to(w, -mu, d);
+#pragma unroll
+        for (int j = 0; j < Elem<T>::kPer; j += 2) {
+            const float e0 = ex2(d[j] * c2), e1 = ex2(d[j + 1] * c2);
+            s0 += e0;
+            s1 += e1;
+            if constexpr (kW) {
+                w0 = fmaf(e0, fmaxf(d[j], low), w0);
+                w1 = fmaf(e1, fmaxf(d[j + 1], low), w1);
+            }
+        }
+    });
+    st.s += s0 + s1;
+    st.w += w0 + w1;
+}
+
+// The triples of up to 32 lanes as one (the same in every lane).
+template <bool kW>
+__device__ __forceinline__ Stats join_lanes(float m, float s, float w, float c2, float low) {
+    const float M = warp_max(m);
+    const float d = m - (M == -kInf ? 0.f : M), f = ex2(d * c2);
+    Stats r{M, warp_sum(f * s), 0.f};
+    if constexpr (kW) r.w = warp_sum(f * (w + s * fmaxf(d, low)));
+    return r;
+}
+
+template <int TH>
+__device__ __forceinline__ void group_sync() {
+    if constexpr (TH == 32) __syncwarp();
+    else __syncthreads();
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// Where a group's warps, and a cluster's CTAs, leave their triples. The CTAs' slots alternate
+// between rows: a CTA may push its next row's triple while another still reads this row's.
+template <int TH>
+struct Joint {
+    float warp[3][TH / 32];
+    float cta[2][3][kMaxCluster];
+};
+
+// The row's statistics in every thread of every CTA that shares it. Contains the group's
+// barrier (before it, threads may leave what the others need after it in shared memory).
+template <int TH, bool kW>
+__device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int cluster, int rank,
+                                          int parity, float c2, float low) {
+    st.s = warp_sum(st.s);
+    if constexpr (kW) st.w = warp_sum(st.w);
+    if constexpr (TH == 32) {
+        group_sync<TH>();
+        return st;
+    } else {
+        const int lane = tid & 31;
+        constexpr int NW = TH / 32;
+        if (lane == 0) {
+            j.warp[0][tid / 32] = st.m;
+            j.warp[1][tid / 32] = st.s;
+            if constexpr (kW) j.warp[2][tid / 32] = st.w;
+        }
+        group_sync<TH>();
+        const bool in = lane < NW;
+        st = join_lanes<kW>(in ? j.warp[0][lane] : -kInf, in ? j.warp[1][lane] : 0.f,
+                            kW && in ? j.warp[2][lane] : 0.f, c2, low);
+        if (cluster > 1) {
+            if (tid < cluster) {  // lane q gives CTA q this CTA's triple
+                const uint32_t to = cluster_map(smem_u32(&j.cta[parity][0][rank]), tid);
+                st_cluster_f32(to, st.m);
+                st_cluster_f32(to + 4 * kMaxCluster, st.s);
+                if constexpr (kW) st_cluster_f32(to + 8 * kMaxCluster, st.w);
+            }
+            cluster_sync();
+            const bool c_in = lane < cluster;
+            st = join_lanes<kW>(c_in ? j.cta[parity][0][lane] : -kInf,
+                                c_in ? j.cta[parity][1][lane] : 0.f,
+                                kW && c_in ? j.cta[parity][2][lane] : 0.f, c2, low);
+        }
+        return st;
+    }
+}
+
+// Registers for a row's vectors: 16 a thread where a warp has a float32 row, so that it holds
+// the audio streams' 2048 logits like a bf16 row's; 8 otherwise.
+template <typename T, int TH>
+__host__ __device__ constexpr int vectors_of() { return TH == 32 && sizeof(T) == 4 ? 16 : 8; }
+
+// CTAs per SM a kernel is compiled for: 64 registers a thread (128 where 64 hold the row).
+template <typename T, int TH>
+__host__ __device__ constexpr int blocks_of() {
+    return TH == 32 ? (sizeof(T) == 4 ? 2 : 4) : 1024 / TH;
+}
+
+template <int TH>
+__host__ __device__ constexpr int block_of() { return TH == 32 ? 256 : TH; }  // warps of short rows share a CTA
+
+// ------------------------------------------------------------------ host side
+
+struct Shape {
+    int threads, cluster;
+};
+
+// Threads and CTAs for a row of V elements: as few threads as hold it in registers, then
+// clusters of 512-thread CTAs; rows of a small batch are spread over more CTAs.
+inline Shape shape_of(int64_t rows, int V, int size, bool warp_ok) {
+    const int per = 16 / size;
+    const int vecs = (V + per - 1) / per + 1;  // rows off a 16-byte boundary have one more
+    if (warp_ok && (V + per - 1) / per <= 32 * (size == 4 ? 16 : 8)) return {32, 1};
+    int cluster = 1;
+    while (cluster < kMaxCluster && vecs > cluster * 512 * 8) cluster *= 2;
+    while (cluster < kMaxCluster && rows * cluster * 2 <= 148 && vecs >= cluster * 2 * 256)
+        cluster *= 2;
+    const int each = (vecs + cluster - 1) / cluster;
+    return {each <= 128 * 8 ? 128 : each <= 256 * 8 ? 256 : 512, cluster};
+}
+
+inline bool on_device(const void* p, size_t align, int dev) {
+    if (!p || (reinterpret_cast<uintptr_t>(p) % align) != 0) return false;
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == dev);
+}
+inline bool maybe_on_device(const void* p, size_t align, int dev) {
+    return p == nullptr || on_device(p, align, dev);
+}
+
+inline int status_of(cudaError_t e) {
+    if (e == cudaSuccess) return MIMI_RVQ_OK;
+    cudaGetLastError();
+    return MIMI_RVQ_ECUDA;
+}
+
+inline bool rows_ok(int dtype, int64_t S, int n, int V, int64_t ss, int64_t sn, float scale) {
+    if (dtype != MIMI_RVQ_F32 && dtype != MIMI_RVQ_BF16) return false;
+    if (S < 0 || n < 0 || n > 65536 || S > (int64_t(1) << 40)) return false;
+    if (V < 1 || V > MIMI_RVQ_MAX_VOCAB || ss < 0 || sn < 0) return false;
+    if ((__int128)ss * S + (__int128)sn * n > ((__int128)1 << 58)) return false;  // no offset wraps
+    return scale > 0.f && scale < kInf;
+}
+
+// Rows of a gradient must not share memory: the smaller stride holds a row, the larger one all
+// rows of the smaller.
+inline bool rows_apart(int64_t S, int n, int V, int64_t ss, int64_t sn) {
+    if (S <= 1) return n <= 1 || sn >= V;
+    if (n <= 1) return ss >= V;
+    if (sn <= ss) return sn >= V && ss >= sn * (n - 1) + V;
+    return ss >= V && sn >= ss * (S - 1) + V;
+}
+
+// The gradient may take the logits' own place (same pointer and strides) but may not overlap
+// them in another way.
+inline bool apart_or_same(const void* x, int64_t ss, int64_t sn, const void* d, int64_t dss,
+                          int64_t dsn, int64_t S, int n, int V, int size) {
+    if (x == d) return (S <= 1 || ss == dss) && (n <= 1 || sn == dsn);
+    const char* a = static_cast<const char*>(x);
+    const char* b = static_cast<const char*>(d);
+    const char* a1 = a + (ss * (S - 1) + sn * (n - 1) + V) * size;
+    const char* b1 = b + (dss * (S - 1) + dsn * (n - 1) + V) * size;
+    return a1 <= b || b1 <= a;
+}
+
+// One launch over all rows: a CTA takes 256 / 32 rows of a warp each, one row, or a
+// cluster's share of one.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_rows(void (*kernel)(KArgs...), int threads, const RowsIn& in, int smem,
+                        cudaStream_t stream, Args... args) {
+    const int block = threads == 32 ? 256 : threads;
+    const int64_t groups = threads == 32 ? (in.rows + 7) / 8 : in.rows;
+    const int64_t most = int64_t(1) << 27;  // the kernels loop over the rest
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((groups < most ? groups : most) * in.cluster));
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = in.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = in.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace logits
+}  // namespace mimi
