@@ -371,27 +371,35 @@ TokenLogprobs = collections.namedtuple("TokenLogprobs",
                                        "logprob entropy lse top_ids top_logprob")
 TokenLogprobs.__doc__ = """Values of token_logprobs: logprob, entropy, lse [S(, n)] float32,
 top_ids [S(, n), k] int32 and top_logprob [S(, n), k] float32; None where not wanted."""
+_NO_VALUES = TokenLogprobs(None, None, None, None, None)
 
 
-class _on:
-    """Run a call on `device` and `stream` (None: the device's current stream), so that its
-    outputs are allocated there too."""
+def _call_on(device, stream, call):
+    """call(raw stream) on `device` and `stream` (None: the device's current stream), which are
+    made current first where they are not, so that outputs are allocated there too."""
+    import torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            if stream.device == device:
+                return call(stream.cuda_stream)
+            with torch.cuda.device(device):
+                return call(stream.cuda_stream)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream().cuda_stream)
+    return call(torch._C._cuda_getCurrentRawStream(device.index))
 
-    def __init__(self, device, stream):
-        import torch
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _values_for(logits, lead, tokens, top_k):
+    """Outputs of token_logprobs: one allocation for the values, one for the lists."""
+    import torch
+    f32 = torch.float32
+    v = logits.new_empty((3, *lead), dtype=f32).unbind(0)
+    if not top_k:
+        return TokenLogprobs(None if tokens is None else v[0], v[1], v[2], None, None)
+    top = logits.new_empty((2, *lead, top_k), dtype=f32).unbind(0)
+    return TokenLogprobs(None if tokens is None else v[0], v[1], v[2], top[0].view(torch.int32),
+                         top[1])
 
 
 def _logit_rows(logits):
@@ -423,18 +431,17 @@ def _row_array(t, shape, dtype, device):
 
 
 def _bad_counter(n_bad, device):
-    import torch
     if n_bad is None:
         return None
+    import torch
     assert n_bad.dtype == torch.int64 and n_bad.numel() >= 1 and n_bad.device == device
     return n_bad.data_ptr()
 
 
 def _gradient(out, logits):
     """The gradient's tensor and its (stride_s, stride_n)."""
-    import torch
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = logits.new_empty(logits.shape)
     assert out.shape == logits.shape and out.dtype == logits.dtype and out.device == logits.device
     st = out.stride()
     assert out.shape[-1] <= 1 or st[-1] == 1
@@ -452,23 +459,21 @@ def token_logprobs(logits, tokens=None, pad=-1, scale=1.0, top_k=0, out=None, n_
     counting tokens past V."""
     import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
-    dev, f32 = logits.device, torch.float32
-    with _on(dev, stream):
-        if out is None:
-            e = torch.empty
-            out = TokenLogprobs(e(lead, dtype=f32, device=dev) if tokens is not None else None,
-                                e(lead, dtype=f32, device=dev), e(lead, dtype=f32, device=dev),
-                                e((*lead, top_k), dtype=torch.int32, device=dev) if top_k else None,
-                                e((*lead, top_k), dtype=f32, device=dev) if top_k else None)
+    dev, f32, top_k = logits.device, torch.float32, int(top_k)
+    tok = _row_tokens(tokens, lead, dev)
+
+    def call(raw):
+        r = _values_for(logits, lead, tokens, max(top_k, 0)) if out is None else out
         top = (*lead, top_k)
         _check(library().mimi_rvq_token_logprob(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, lead, dev), int(pad),
-            float(scale), int(top_k), _row_array(out.logprob, lead, f32, dev),
-            _row_array(out.entropy, lead, f32, dev), _row_array(out.lse, lead, f32, dev),
-            _row_array(out.top_ids, top, torch.int32, dev),
-            _row_array(out.top_logprob, top, f32, dev), _bad_counter(n_bad, dev),
-            _stream(stream)), "mimi_rvq_token_logprob")
-    return out
+            logits.data_ptr(), dt, S, n, V, ss, sn, *tok, pad, scale, top_k,
+            _row_array(r.logprob, lead, f32, dev), _row_array(r.entropy, lead, f32, dev),
+            _row_array(r.lse, lead, f32, dev), _row_array(r.top_ids, top, torch.int32, dev),
+            _row_array(r.top_logprob, top, f32, dev), _bad_counter(n_bad, dev), raw),
+            "mimi_rvq_token_logprob")
+        return r
+
+    return _call_on(dev, stream, call)
 
 
 def token_logprobs_grad(logits, tokens=None, g_logprob=None, g_entropy=None, g_lse=None, pad=-1,
@@ -481,23 +486,22 @@ def token_logprobs_grad(logits, tokens=None, g_logprob=None, g_entropy=None, g_l
     import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
     dev, f32 = logits.device, torch.float32
-    with _on(dev, stream):
-        out, d_strides = _gradient(out, logits)
-        v = TokenLogprobs(None, None, None, None, None) if not values else values
-        if values is True:
-            e = torch.empty
-            v = TokenLogprobs(e(lead, dtype=f32, device=dev) if tokens is not None else None,
-                              e(lead, dtype=f32, device=dev), e(lead, dtype=f32, device=dev),
-                              None, None)
+    tok = _row_tokens(tokens, lead, dev)
+
+    def call(raw):
+        d, d_strides = _gradient(out, logits)
+        v = _values_for(logits, lead, tokens, 0) if values is True else (values or _NO_VALUES)
         assert v.top_ids is None and v.top_logprob is None, "the gradient call lists no tokens"
         _check(library().mimi_rvq_token_logprob_grad(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, lead, dev), int(pad),
-            float(scale), _row_array(g_logprob, lead, f32, dev),
-            _row_array(g_entropy, lead, f32, dev), _row_array(g_lse, lead, f32, dev),
-            out.data_ptr(), *d_strides, _row_array(v.logprob, lead, f32, dev),
-            _row_array(v.entropy, lead, f32, dev), _row_array(v.lse, lead, f32, dev),
-            _bad_counter(n_bad, dev), _stream(stream)), "mimi_rvq_token_logprob_grad")
-    return (out, v) if values else out
+            logits.data_ptr(), dt, S, n, V, ss, sn, *tok, pad, scale,
+            _row_array(g_logprob, lead, f32, dev), _row_array(g_entropy, lead, f32, dev),
+            _row_array(g_lse, lead, f32, dev), d.data_ptr(), *d_strides,
+            _row_array(v.logprob, lead, f32, dev), _row_array(v.entropy, lead, f32, dev),
+            _row_array(v.lse, lead, f32, dev), _bad_counter(n_bad, dev), raw),
+            "mimi_rvq_token_logprob_grad")
+        return (d, v) if values else d
+
+    return _call_on(dev, stream, call)
 
 
 def _teacher_list(ids, teacher, lead, device):
@@ -517,15 +521,18 @@ def distill_topk(logits, ids, teacher, tail=False, scale=1.0, out=None, n_bad=No
     class. scale applies to the student only."""
     import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
-    dev = logits.device
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(lead, dtype=torch.float32, device=dev)
+    dev, f32 = logits.device, torch.float32
+    lists = _teacher_list(ids, teacher, lead, dev)
+
+    def call(raw):
+        loss = logits.new_empty(lead, dtype=f32) if out is None else out
         _check(library().mimi_rvq_distill_topk(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *_teacher_list(ids, teacher, lead, dev),
-            1 if tail else 0, float(scale), _row_array(out, lead, torch.float32, dev),
-            _bad_counter(n_bad, dev), _stream(stream)), "mimi_rvq_distill_topk")
-    return out
+            logits.data_ptr(), dt, S, n, V, ss, sn, *lists, 1 if tail else 0, scale,
+            _row_array(loss, lead, f32, dev), _bad_counter(n_bad, dev), raw),
+            "mimi_rvq_distill_topk")
+        return loss
+
+    return _call_on(dev, stream, call)
 
 
 def distill_topk_grad(logits, ids, teacher, g=None, tail=False, scale=1.0, loss=None, out=None,
@@ -537,13 +544,16 @@ def distill_topk_grad(logits, ids, teacher, g=None, tail=False, scale=1.0, loss=
     import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
     dev, f32 = logits.device, torch.float32
-    with _on(dev, stream):
-        out, d_strides = _gradient(out, logits)
-        if loss is True:
-            loss = torch.empty(lead, dtype=f32, device=dev)
+    lists = _teacher_list(ids, teacher, lead, dev)
+
+    def call(raw):
+        d, d_strides = _gradient(out, logits)
+        losses = logits.new_empty(lead, dtype=f32) if loss is True else loss
         _check(library().mimi_rvq_distill_topk_grad(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *_teacher_list(ids, teacher, lead, dev),
-            1 if tail else 0, float(scale), _row_array(g, lead, f32, dev), out.data_ptr(),
-            *d_strides, _row_array(loss, lead, f32, dev), _bad_counter(n_bad, dev),
-            _stream(stream)), "mimi_rvq_distill_topk_grad")
-    return out if loss is None else (out, loss)
+            logits.data_ptr(), dt, S, n, V, ss, sn, *lists, 1 if tail else 0, scale,
+            _row_array(g, lead, f32, dev), d.data_ptr(), *d_strides,
+            _row_array(losses, lead, f32, dev), _bad_counter(n_bad, dev), raw),
+            "mimi_rvq_distill_topk_grad")
+        return d if losses is None else (d, losses)
+
+    return _call_on(dev, stream, call)

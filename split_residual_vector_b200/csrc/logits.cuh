@@ -9,9 +9,9 @@
 // Up to NV vectors per thread are kept in registers, so a gradient reads its
 // row once; a longer part is walked in chunks of TH * NV vectors.
 //
-// Every statistic comes from m = max x, s = sum e^{c (x - m)} and
-// w = sum e^{c (x - m)} (x - m), c = scale, all in float32:
-//     lse = c m + ln s,  ln p_i = c (x_i - m) - ln s,  entropy = ln s - c w / s.
+// Every statistic comes from m = max x, s = sum 2^t_i and w = sum 2^t_i t_i with
+// t_i = log2(e) c (x_i - m), c = scale, all in float32:
+//     lse = c m + ln s,  ln p_i = c (x_i - m) - ln s,  entropy = ln s - ln 2 w / s.
 // Each warp sums against its own maximum (one hardware reduction), so a row
 // needs one barrier, where the warps' triples are joined; a row split over a
 // cluster needs one cluster barrier more.
@@ -32,7 +32,7 @@ namespace logits {
 constexpr int kMaxTop = MIMI_RVQ_MAX_TOP;
 constexpr int kMaxCluster = 8;  // CTAs that may share a row (the portable cluster size)
 constexpr float kInf = INFINITY;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kFull = 0xffffffffu;
 
 // The rows of a logits tensor [S][n][V]; strides in elements.
@@ -72,22 +72,6 @@ __device__ __forceinline__ float element(const uint32_t (&w)[4], int j) {
     else return __uint_as_float((j & 1) ? (w[j / 2] & 0xFFFF0000u) : (w[j / 2] << 16));
 }
 
-// a vector's elements plus `a` (one rounding each; bf16 widens exactly)
-__device__ __forceinline__ void add_to(const uint32_t (&w)[4], float a, float (&d)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = __uint_as_float(w[j]) + a;
-}
-__device__ __forceinline__ void add_to(const uint32_t (&w)[4], float a, float (&d)[8]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        asm("{\n\t.reg .b16 lo, hi;\n\t"
-            "mov.b32 {lo, hi}, %2;\n\t"
-            "add.rn.f32.bf16 %0, lo, %3;\n\t"
-            "add.rn.f32.bf16 %1, hi, %3;\n\t}"
-            : "=f"(d[2 * j]), "=f"(d[2 * j + 1])
-            : "r"(w[j]), "f"(a));
-}
-
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -112,17 +96,118 @@ __device__ __forceinline__ V warp_sum(V v) {
     return v;
 }
 
-// A difference x - max below this has probability 0 in float32 (e^-200); clamping it there keeps
-// 0 times -inf out of the products with a probability.
-__device__ __forceinline__ float far_below(float c) { return fmaxf(-200.f / c, -3.0e38f); }
+// Two float32 values in a 64-bit register pair and the instructions that work on both.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void halves(Pair p, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair ex2_pair(Pair t) {
+    float a, b;
+    halves(t, a, b);
+    return pair_of(ex2(a), ex2(b));
+}
+// max that keeps NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
-// ln p of a logit of the row; the difference and product in float64, so that logits of opposite
-// sign near float32's limits do not overflow (a few of these per row).
+// Exponents t = log2(e) c (x - m) of a row's or warp's logits, 2^t = e^{c (x - m)}.
+// Near: t = x c2 - ref in one fused multiply-add per logit, ref = m c2 rounded; t is then off by
+// the same `shift` = m c2 - ref for every logit, at most 2^-9, which is taken back from the sums.
+// Far (logits or scales beyond that): the difference first, then the product. With kFinite, t is
+// at least -236 (2^t is 0 there too), so that 0 t is 0 for a logit of -inf; bf16 logits are
+// clamped as pairs before they are widened.
+constexpr float kLow = -300.f;
+struct Scale {
+    float c2, m, ref, shift;
+    uint32_t floor_bf16x2;
+    bool far;
+
+    __device__ Scale(float c2_, float m_) : c2(c2_), m(m_ == -kInf ? 0.f : m_) {
+        ref = m * c2;
+        far = !(fabsf(ref) < 32768.f && c2 > 1.0e-33f && c2 < 1.0e30f);
+        shift = far ? 0.f : fmaf(m, c2, -ref);
+        const float f = __fdividef(ref + kLow, c2);
+        floor_bf16x2 = far ? 0xFF80FF80u : pack_bf16x2(f, f);  // far: no floor here
+    }
+};
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T, bool kFinite>
+__device__ __forceinline__ void exponents(const uint32_t (&w)[4], const Scale& k,
+                                          Pair (&t)[Elem<T>::kPer / 2]) {
+    constexpr int kPairs = Elem<T>::kPer / 2;
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+        if constexpr (sizeof(T) == 4) {
+            t[j] = pair_of(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+        } else {
+            const uint32_t u = kFinite ? max_nan_bf16x2(w[j], k.floor_bf16x2) : w[j];
+            t[j] = pair_of(bf16_lo_to_f32(u), bf16_hi_to_f32(u));
+        }
+    }
+    if (!k.far) {
+        const Pair c = pair_of(k.c2, k.c2), r = pair_of(-k.ref, -k.ref);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) t[j] = fma2(t[j], c, r);
+    } else {
+        const Pair c = pair_of(k.c2, k.c2), m = pair_of(-k.m, -k.m);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) t[j] = mul2(add2(t[j], m), c);
+    }
+    if (kFinite && (sizeof(T) == 4 || k.far))
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            float a, b;
+            halves(t[j], a, b);
+            t[j] = pair_of(max_nan(a, kLow), max_nan(b, kLow));
+        }
+}
+// the same for one logit, without the near form
+__device__ __forceinline__ float exponent(float x, float m, float c2) {
+    return max_nan((x - (m == -kInf ? 0.f : m)) * c2, kLow);
+}
+
+// ln p of a logit of the row. Logits of opposite sign near float32's limits, whose difference or
+// product overflows, are taken in float64.
 __device__ __forceinline__ float log_prob(float x, float c, float m, float ln_s) {
+    const float d = c * (x - m);
+    if (fabsf(d) < 1.0e38f) return fmaf(c, x - m, -ln_s);
     return (float)((double)c * ((double)x - (double)m) - (double)ln_s);
 }
 
 // ------------------------------------------------------------------ rows
+
+// Step and stream of a row.
+__device__ __forceinline__ void split_row(int64_t r, int n, int64_t& s, int& j) {
+    s = n == 1 ? r : (r >> 32) == 0 ? (int64_t)((uint32_t)r / (uint32_t)n) : r / n;
+    j = (int)(r - s * n);
+}
 
 // One thread group's share of a row: vectors [v0, v1), of which [lo, hi) lie wholly in the row.
 template <typename T>
@@ -137,7 +222,7 @@ struct Part {
     __device__ Part(const T* row, int V_, int rank, int cluster) : x(row), V(V_) {
         a = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
         const int all = (a + V + kPer - 1) / kPer;
-        const int per = (all + cluster - 1) / cluster;
+        const int per = (all + cluster - 1) >> (31 - __clz(cluster));  // a power of two
         v0 = min(rank * per, all);
         v1 = min(v0 + per, all);
         lo = max(v0, a ? 1 : 0);
@@ -279,15 +364,26 @@ __device__ __forceinline__ void each_vector(uint32_t (&v)[NV][4], int here, int 
         if (i * TH + (tid & ~31) < here) f(i, v[i]);
 }
 
+template <typename T>
+__device__ __forceinline__ float vector_max(const uint32_t (&w)[4]) {
+    if constexpr (sizeof(T) == 4) {
+        return fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                     fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+    } else {
+        const uint32_t a = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
+        return fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a));
+    }
+}
+
 struct Stats {
-    float m, s, w;  // m is -inf where no logit is finite
+    float m, s, w;  // m is -inf where no logit is above it
 };
 
 // Adds a chunk to a warp's running statistics: m is the warp's, s and w are the thread's.
-// top: the thread's own maximum over all chunks.
+// Returns the thread's own maximum in the chunk.
 template <int TH, int NV, bool kW, typename T>
-__device__ __forceinline__ void add_chunk(uint32_t (&v)[NV][4], int here, int tid, float c2,
-                                          float low, Stats& st, float& top) {
+__device__ __forceinline__ float add_chunk(uint32_t (&v)[NV][4], int here, int tid, float c2,
+                                           Stats& st) {
     float mx;
     if constexpr (sizeof(T) == 4) {
         mx = -kInf;
@@ -302,41 +398,45 @@ __device__ __forceinline__ void add_chunk(uint32_t (&v)[NV][4], int here, int ti
         });
         mx = fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a));
     }
-    top = fmaxf(top, mx);
     const float m = fmaxf(st.m, warp_max(mx));
-    const float mu = m == -kInf ? 0.f : m;
+    const Scale k(c2, m);
     if (st.m != m && st.m != -kInf) {  // an earlier chunk's sums move to the new maximum
-        const float d = st.m - m, f = ex2(d * c2);
-        if constexpr (kW) st.w = f * (st.w + st.s * fmaxf(d, low));
+        const float t = exponent(st.m, m, c2), f = ex2(t);
+        if constexpr (kW) st.w = f * fmaf(st.s, t, st.w);
         st.s *= f;
     }
     st.m = m;
-    float s0 = 0.f, s1 = 0.f, w0 = 0.f, w1 = 0.f;
+    Pair s2 = 0, w2 = 0;  // (0, 0)
     each_vector<TH, NV>(v, here, tid, [&](int, uint32_t (&w)[4]) {
-        float d[Elem<T>::kPer];
-        add_to(w, -mu, d);
+        Pair t[Elem<T>::kPer / 2];
+        exponents<T, kW>(w, k, t);
 #pragma unroll
-        for (int j = 0; j < Elem<T>::kPer; j += 2) {
-            const float e0 = ex2(d[j] * c2), e1 = ex2(d[j + 1] * c2);
-            s0 += e0;
-            s1 += e1;
-            if constexpr (kW) {
-                w0 = fmaf(e0, fmaxf(d[j], low), w0);
-                w1 = fmaf(e1, fmaxf(d[j + 1], low), w1);
-            }
+        for (int j = 0; j < Elem<T>::kPer / 2; ++j) {
+            const Pair e = ex2_pair(t[j]);
+            s2 = add2(s2, e);
+            if constexpr (kW) w2 = fma2(e, t[j], w2);
         }
     });
-    st.s += s0 + s1;
-    st.w += w0 + w1;
+    float s, s1, w = 0.f, w1 = 0.f;
+    halves(s2, s, s1);
+    s += s1;
+    if constexpr (kW) {
+        halves(w2, w, w1);
+        w += w1;
+    }
+    const float back = ex2(-k.shift);
+    st.s = fmaf(s, back, st.s);
+    if constexpr (kW) st.w = fmaf(fmaf(-k.shift, s, w), back, st.w);
+    return mx;
 }
 
 // The triples of up to 32 lanes as one (the same in every lane).
 template <bool kW>
-__device__ __forceinline__ Stats join_lanes(float m, float s, float w, float c2, float low) {
+__device__ __forceinline__ Stats join_lanes(float m, float s, float w, float c2) {
     const float M = warp_max(m);
-    const float d = m - (M == -kInf ? 0.f : M), f = ex2(d * c2);
+    const float t = exponent(m, M, c2), f = ex2(t);
     Stats r{M, warp_sum(f * s), 0.f};
-    if constexpr (kW) r.w = warp_sum(f * (w + s * fmaxf(d, low)));
+    if constexpr (kW) r.w = warp_sum(f * fmaf(s, t, w));
     return r;
 }
 
@@ -355,6 +455,9 @@ __device__ __forceinline__ void cluster_wait() {
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
@@ -367,11 +470,10 @@ struct Joint {
     float cta[2][3][kMaxCluster];
 };
 
-// The row's statistics in every thread of every CTA that shares it. Contains the group's
-// barrier (before it, threads may leave what the others need after it in shared memory).
+// The group's statistics in every thread of it. Contains the group's barrier (before it, threads
+// may leave what the others need after it in shared memory).
 template <int TH, bool kW>
-__device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int cluster, int rank,
-                                          int parity, float c2, float low) {
+__device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, float c2) {
     st.s = warp_sum(st.s);
     if constexpr (kW) st.w = warp_sum(st.w);
     if constexpr (TH == 32) {
@@ -387,23 +489,41 @@ __device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int c
         }
         group_sync<TH>();
         const bool in = lane < NW;
-        st = join_lanes<kW>(in ? j.warp[0][lane] : -kInf, in ? j.warp[1][lane] : 0.f,
-                            kW && in ? j.warp[2][lane] : 0.f, c2, low);
-        if (cluster > 1) {
-            if (tid < cluster) {  // lane q gives CTA q this CTA's triple
-                const uint32_t to = cluster_map(smem_u32(&j.cta[parity][0][rank]), tid);
-                st_cluster_f32(to, st.m);
-                st_cluster_f32(to + 4 * kMaxCluster, st.s);
-                if constexpr (kW) st_cluster_f32(to + 8 * kMaxCluster, st.w);
-            }
-            cluster_sync();
-            const bool c_in = lane < cluster;
-            st = join_lanes<kW>(c_in ? j.cta[parity][0][lane] : -kInf,
-                                c_in ? j.cta[parity][1][lane] : 0.f,
-                                kW && c_in ? j.cta[parity][2][lane] : 0.f, c2, low);
-        }
-        return st;
+        return join_lanes<kW>(in ? j.warp[0][lane] : -kInf, in ? j.warp[1][lane] : 0.f,
+                              kW && in ? j.warp[2][lane] : 0.f, c2);
     }
+}
+
+// Gives CTA `to` of the cluster this CTA's triple.
+template <int TH, bool kW>
+__device__ __forceinline__ void push_stats(Joint<TH>& j, const Stats& st, int rank, int to,
+                                           int parity) {
+    const uint32_t at = cluster_map(smem_u32(&j.cta[parity][0][rank]), to);
+    st_cluster_f32(at, st.m);
+    st_cluster_f32(at + 4 * kMaxCluster, st.s);
+    if constexpr (kW) st_cluster_f32(at + 8 * kMaxCluster, st.w);
+}
+// The triples that the cluster's CTAs pushed, as one.
+template <int TH, bool kW>
+__device__ __forceinline__ Stats join_cluster(const Joint<TH>& j, int tid, int cluster, int parity,
+                                              float c2) {
+    const int lane = tid & 31;
+    const bool in = lane < cluster;
+    return join_lanes<kW>(in ? j.cta[parity][0][lane] : -kInf, in ? j.cta[parity][1][lane] : 0.f,
+                          kW && in ? j.cta[parity][2][lane] : 0.f, c2);
+}
+
+// The row's statistics in every thread of every CTA that shares it.
+template <int TH, bool kW>
+__device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int cluster, int rank,
+                                          int parity, float c2) {
+    st = join_group<TH, kW>(j, st, tid, c2);
+    if (cluster > 1) {
+        if (tid < cluster) push_stats<TH, kW>(j, st, rank, tid, parity);
+        cluster_sync();
+        st = join_cluster<TH, kW>(j, tid, cluster, parity, c2);
+    }
+    return st;
 }
 
 // Registers for a row's vectors: 16 a thread where a warp has a float32 row, so that it holds
@@ -414,7 +534,7 @@ __host__ __device__ constexpr int vectors_of() { return TH == 32 && sizeof(T) ==
 // CTAs per SM a kernel is compiled for: 64 registers a thread (128 where 64 hold the row).
 template <typename T, int TH>
 __host__ __device__ constexpr int blocks_of() {
-    return TH == 32 ? (sizeof(T) == 4 ? 2 : 4) : 1024 / TH;
+    return TH == 32 ? (sizeof(T) == 4 ? 2 : 3) : 1024 / TH;
 }
 
 template <int TH>
@@ -426,18 +546,21 @@ struct Shape {
     int threads, cluster;
 };
 
-// Threads and CTAs for a row of V elements: as few threads as hold it in registers, then
-// clusters of 512-thread CTAs; rows of a small batch are spread over more CTAs.
-inline Shape shape_of(int64_t rows, int V, int size, bool warp_ok) {
+// Threads and CTAs for a row of V elements. hold: the row stays in registers between two passes,
+// so it takes as many threads as that needs, then clusters of 512-thread CTAs; a row that is
+// read once is walked in chunks by 256 threads, four CTAs a SM, so that some load while others
+// join their sums. Rows of a small batch are spread over more CTAs.
+inline Shape shape_of(int64_t rows, int V, int size, bool warp_ok, bool hold) {
     const int per = 16 / size;
     const int vecs = (V + per - 1) / per + 1;  // rows off a 16-byte boundary have one more
     if (warp_ok && (V + per - 1) / per <= 32 * (size == 4 ? 16 : 8)) return {32, 1};
     int cluster = 1;
-    while (cluster < kMaxCluster && vecs > cluster * 512 * 8) cluster *= 2;
+    while (hold && cluster < kMaxCluster && vecs > cluster * 512 * 8) cluster *= 2;
     while (cluster < kMaxCluster && rows * cluster * 2 <= 148 && vecs >= cluster * 2 * 256)
         cluster *= 2;
     const int each = (vecs + cluster - 1) / cluster;
-    return {each <= 128 * 8 ? 128 : each <= 256 * 8 ? 256 : 512, cluster};
+    if (each <= 128 * 8) return {128, cluster};
+    return {each <= 256 * 8 || !hold ? 256 : 512, cluster};
 }
 
 inline bool on_device(const void* p, size_t align, int dev) {
@@ -495,7 +618,15 @@ cudaError_t launch_rows(void (*kernel)(KArgs...), int threads, const RowsIn& in,
                         cudaStream_t stream, Args... args) {
     const int block = threads == 32 ? 256 : threads;
     const int64_t groups = threads == 32 ? (in.rows + 7) / 8 : in.rows;
-    const int64_t most = int64_t(1) << 27;  // the kernels loop over the rest
+    int64_t most = int64_t(1) << 27;  // the kernels loop over the rest
+    if (threads == 32) {              // as many CTAs as are resident: each sets up once
+        int dev = 0, sms = 148, per_sm = 4;
+        if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (groups > (int64_t)sms * 2)
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block, smem);
+        most = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((groups < most ? groups : most) * in.cluster));
     cfg.blockDim = dim3(block);

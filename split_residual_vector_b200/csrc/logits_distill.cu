@@ -67,14 +67,15 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
     const int tid = TH == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int group = TH == 32 ? threadIdx.x / 32 : 0;
     const int rank = in.cluster > 1 ? (int)cluster_ctarank() : 0;
-    const float c2 = in.c * kLog2e, low = far_below(in.c);
+    const float c2 = in.c * kLog2e;
     ListShared& ls = lists[group];
     int parity = 0;
     if (in.cluster > 1) cluster_sync();
     for (int64_t r = (int64_t)(blockIdx.x / in.cluster) * kRows + group; r < in.rows;
          r += (int64_t)(gridDim.x / in.cluster) * kRows) {
-        const int64_t s = r / in.n;
-        const int j = (int)(r - s * in.n);
+        int64_t s;
+        int j;
+        split_row(r, in.n, s, j);
         const Part<T> p(static_cast<const T*>(in.x) + s * in.ss + j * in.sn, in.V, rank, in.cluster);
         const int chunks = (p.size() + TH * NV - 1) / (TH * NV);
         uint8_t* mark = marks + (size_t)group * most_chunks<T, TH>(in.V, in.cluster) * TH * NV;
@@ -192,19 +193,18 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
         Stats rest{-kInf, 0.f, 0.f}, all{-kInf, 0.f, 0.f};
         const bool empty = ls.present == 0;
         if (!skip && !empty) {
-            float top = -kInf;
             for (int q2 = 0; q2 < chunks; ++q2) {
                 const int base = p.v0 + q2 * TH * NV;
                 if (q2) load_chunk<TH, NV>(p, base, tid, v);
                 hide<NV, T>(mark + (q2 * TH + tid) * NV, v);
-                add_chunk<TH, NV, false, T>(v, p.v1 - base, tid, c2, low, rest, top);
+                add_chunk<TH, NV, false, T>(v, p.v1 - base, tid, c2, rest);
             }
             if (in.cluster > 1 && tid < in.cluster) {
                 const uint32_t to = cluster_map(smem_u32(&listed_of.cta[parity][0][rank]), tid);
                 st_cluster_f32(to, ls.m);
                 st_cluster_f32(to + 4 * kMaxCluster, ls.s);
             }
-            rest = join_row<TH, false>(joint[group], rest, tid, in.cluster, rank, parity, c2, low);
+            rest = join_row<TH, false>(joint[group], rest, tid, in.cluster, rank, parity, c2);
             float lm = ls.m, lsum = ls.s;
             parity ^= 1;
             if (in.cluster > 1) {
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
                 const bool in_c = lane < in.cluster;
                 const Stats l = join_lanes<false>(in_c ? listed_of.cta[parity ^ 1][0][lane] : -kInf,
                                                   in_c ? listed_of.cta[parity ^ 1][1][lane] : 0.f, 0.f,
-                                                  c2, low);
+                                                  c2);
                 lm = l.m;
                 lsum = l.s;
             }
@@ -241,11 +241,11 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
             const bool wide =
                 ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(p.x)) & 15u) == 0;
             const float gc = g * in.c, inv = none ? 0.f : 1.f / all.s;
-            const float mr = rest.m == -kInf ? 0.f : rest.m;
-            // a rest of -inf only has no gradient of its own: e^{...} is 0 there
+            const Scale k(c2, rest.m);
+            // a rest of -inf only has no gradient of its own: 2^t is 0 there
             const float f = none ? 0.f
-                : gc * (Q * inv * (rest.s == 0.f ? 1.f : ex2((rest.m - all.m) * c2))
-                        - (qr > 0.f ? qr / rest.s : 0.f));
+                : gc * ex2(-k.shift) * (Q * inv * (rest.s == 0.f ? 1.f : ex2((rest.m - all.m) * c2))
+                                        - (qr > 0.f ? qr / rest.s : 0.f));
             for (int q2 = 0; q2 < chunks; ++q2) {
                 const int base = p.v0 + q2 * TH * NV;
                 if (!none && chunks > 1) {
@@ -259,9 +259,11 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
 #pragma unroll
                         for (int e = 0; e < kPer; ++e) y[e] = 0.f;
                     } else {
-                        add_to(w, -mr, y);
+                        Pair t[kPer / 2];
+                        exponents<T, false>(w, k, t);
 #pragma unroll
-                        for (int e = 0; e < kPer; ++e) y[e] = ex2(y[e] * c2) * f;
+                        for (int e = 0; e < kPer / 2; ++e)
+                            halves(mul2(ex2_pair(t[e]), pair_of(f, f)), y[2 * e], y[2 * e + 1]);
                     }
                     store_vector<T>(d, at, y, wide && vec >= p.lo && vec < p.hi, vec < p.v1, in.V);
                 });
@@ -298,8 +300,11 @@ cudaError_t distill_of(const Shape& sh, const RowsIn& in, const TeacherIn& te, c
         case 32: return distill_with<T, kGrad, 32>(in, te, s);
         case 128: return distill_with<T, kGrad, 128>(in, te, s);
         case 256: return distill_with<T, kGrad, 256>(in, te, s);
-        default: return distill_with<T, kGrad, 512>(in, te, s);
+        default: break;
     }
+    // only a gradient holds rows that want 512 threads
+    if constexpr (kGrad) return distill_with<T, kGrad, 512>(in, te, s);
+    return cudaErrorInvalidConfiguration;
 }
 
 int distill(const void* logits, int dtype, int64_t S, int n, int V, int64_t stride_s,
@@ -326,7 +331,7 @@ int distill(const void* logits, int dtype, int64_t S, int n, int V, int64_t stri
                  !apart_or_same(logits, stride_s, stride_n, dlogits, d_stride_s, d_stride_n, S, n,
                                 V, size)))
         return MIMI_RVQ_EINVAL;
-    const Shape sh = shape_of(S * n, V, size, true);
+    const Shape sh = shape_of(S * n, V, size, true, grad);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.cluster};
     const TeacherIn te{ids, teacher, teacher_dtype == MIMI_RVQ_BF16, k, tail, g, loss, dlogits,
                        d_stride_s, d_stride_n, reinterpret_cast<unsigned long long*>(n_bad)};

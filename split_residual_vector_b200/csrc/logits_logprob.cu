@@ -55,15 +55,15 @@ __device__ __forceinline__ uint32_t order_of(float v) {
     const uint32_t b = __float_as_uint(v + 0.f);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-constexpr uint32_t kOrderNegInf = 0x007FFFFFu;  // order_of(-inf); NaN below it does not occur
+constexpr uint32_t kOrderNegInf = 0x007FFFFFu;  // order_of(-inf)
 // Larger comes first: (logit descending, id ascending).
 __device__ __forceinline__ Key key_of(float v, int id) {
     return ((Key)order_of(v) << 32) | (0xFFFFFFFFu - (uint32_t)id);
 }
-__device__ __forceinline__ float key_value(Key key) {
-    const uint32_t o = (uint32_t)(key >> 32);
+__device__ __forceinline__ float order_value(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
+__device__ __forceinline__ float key_value(Key key) { return order_value((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int key_id(Key key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
 // The row's target, -1 if it has none; count: add a token past V to n_bad.
@@ -84,7 +84,7 @@ __device__ __forceinline__ void put_values(const ValuesOut& o, int64_t r, int t,
     const bool none = st.s == 0.f;
     if (o.logprob != nullptr)
         o.logprob[r] = t < 0 ? 0.f : none ? -kInf : log_prob(xt, c, st.m, ln_s);
-    if (o.entropy != nullptr) o.entropy[r] = none ? 0.f : ln_s - c * (st.w / st.s);
+    if (o.entropy != nullptr) o.entropy[r] = none ? 0.f : ln_s - kLn2 * (st.w / st.s);
     if (o.lse != nullptr) o.lse[r] = none ? -kInf : c * st.m + ln_s;
 }
 
@@ -99,120 +99,181 @@ struct TopShared {
     static constexpr int kGroups = TH > 256 ? 256 : TH;  // maxima that bound the k-th logit
     static constexpr int kCap = TH == 32 ? 128 : 1024;
     uint32_t most[TH == 32 ? 1 : kGroups];
-    uint32_t bound;
+    float bound;
     int count;
-    Key list[kCap];
+    alignas(16) Key list[kCap + 8];
     Key last[TH / 32];
+    // the threads' maxima of chunk c (and c + 8, ...), for parts of several chunks
+    float of_chunk[TH == 32 ? 1 : 8][TH == 32 ? 1 : TH];
 };
 template <int TH>
-struct TopLists {  // the sorted lists of a cluster's CTAs, in the first one's memory
+struct TopLists {  // the keys that a cluster's CTAs give its first one
     Key of[TH == 32 ? 1 : kMaxCluster][TH == 32 ? 1 : kMaxTop];
+    int count[kMaxCluster];
 };
 
-// Sorted keys of this part's k largest logits: put(place, key) for places below the number of
-// logits above -inf, put(place, 0) for the others. `v` holds the part where it is one chunk.
-template <int TH, int NV, typename T, typename Put>
-__device__ void part_top(TopShared<TH>& sh, const Part<T>& p, uint32_t (&v)[NV][4], float top,
-                         int tid, int k, Put&& put) {
-    constexpr int kG = TopShared<TH>::kGroups, kCap = TopShared<TH>::kCap;
-    const int lane = tid & 31;
-    const bool one = p.size() <= TH * NV;
-    // the largest bound (in steps of 2^16) that k groups' maxima reach
-    const uint32_t mine = order_of(top);
-    uint32_t g = mine;
-    if constexpr (TH == 32) {
-        uint32_t b = 0;
-        for (int bit = 31; bit >= 16; --bit) {
-            const uint32_t t = b | (1u << bit);
-            if (__popc(__ballot_sync(kFull, g >= t)) >= k) b = t;
+// Leaves the groups' maxima; the group's barrier follows.
+template <int TH>
+__device__ __forceinline__ void leave_maxima(TopShared<TH>& sh, float top, int tid) {
+    constexpr int kShare = TH / TopShared<TH>::kGroups;
+    if constexpr (TH > 32) {
+        uint32_t g = order_of(top);
+#pragma unroll
+        for (int o = 1; o < kShare; o *= 2) g = max(g, __shfl_xor_sync(kFull, g, o));
+        if (tid % kShare == 0) sh.most[tid / kShare] = g;
+    }
+}
+
+// The part's logits that reach the bound, as unordered keys in sh.list: returns their number,
+// at least min(k, the logits above -inf); past kCap the list is not complete. `v` holds the part
+// where it is one chunk.
+template <int TH, int NV, typename T>
+__device__ __forceinline__ int collect(TopShared<TH>& sh, const Part<T>& p, uint32_t (&v)[NV][4],
+                                       float top, int tid, int k) {
+    constexpr int kN = TopShared<TH>::kGroups / 32, kCap = TopShared<TH>::kCap;
+    if (tid < 32) {
+        uint32_t q[kN];
+        uint32_t hi = 0, lo = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            q[i] = TH == 32 ? order_of(top) : sh.most[tid + 32 * i];
+            hi = max(hi, q[i]);
+            lo = min(lo, q[i]);
         }
-        if (lane == 0) {
-            sh.bound = max(b, kOrderNegInf + 1);
+        hi = __reduce_max_sync(kFull, hi);
+        lo = __reduce_min_sync(kFull, lo);
+        // the largest bound, in steps of 2^16, that k maxima reach: bits that all maxima share
+        // are theirs, and k maxima exactly is as good as it gets
+        uint32_t b = 0;
+        if (k <= 32 * kN) {
+            const int top_bit = 31 - __clz(lo ^ hi);  // -1: all are equal
+            b = lo == hi ? lo : lo & ~((2u << top_bit) - 1u);
+            for (int bit = top_bit; bit >= 16; --bit) {
+                const uint32_t t = b | (1u << bit);
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) n += __popc(__ballot_sync(kFull, q[i] >= t));
+                if (n >= k) b = t;
+                if (n == k) break;
+            }
+        }
+        if (tid == 0) {
+            sh.bound = order_value(max(b, kOrderNegInf + 1));
             sh.count = 0;
         }
-        __syncwarp();
-    } else {
+    }
+    group_sync<TH>();
+    const float bound = sh.bound;
+    const int lane = tid & 31;
+    // a chunk's logits (each lane's own) that reach the bound: counted, then given places
+    auto append = [&](int base) {
+        int mine = 0;
 #pragma unroll
-        for (int o = 1; o < TH / kG; o *= 2) g = max(g, __shfl_xor_sync(kFull, g, o));
-        if (tid % (TH / kG) == 0) sh.most[tid / (TH / kG)] = g;
-        __syncthreads();
-        if (tid < 32) {
-            uint32_t q[kG / 32];
+        for (int i = 0; i < NV; ++i) {
+            if (!__any_sync(kFull, vector_max<T>(v[i]) >= bound)) continue;
 #pragma unroll
-            for (int i = 0; i < kG / 32; ++i) q[i] = sh.most[lane + 32 * i];
-            uint32_t b = 0;
-            for (int bit = 31; bit >= 16; --bit) {
-                const uint32_t t = b | (1u << bit);
-                unsigned n = 0;
+            for (int j = 0; j < Part<T>::kPer; ++j) mine += element<T>(v[i], j) >= bound;
+        }
+        int upto = mine;
 #pragma unroll
-                for (int i = 0; i < kG / 32; ++i) n += q[i] >= t;
-                if ((int)__reduce_add_sync(kFull, n) >= k) b = t;
-            }
-            if (lane == 0) {
-                sh.bound = max(b, kOrderNegInf + 1);
-                sh.count = 0;
+        for (int o = 1; o < 32; o *= 2) {
+            const int before = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += before;
+        }
+        int at = 0;
+        if (lane == 31) at = atomicAdd(&sh.count, upto);
+        at = __shfl_sync(kFull, at, 31) + upto - mine;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!__any_sync(kFull, vector_max<T>(v[i]) >= bound)) continue;
+#pragma unroll
+            for (int j = 0; j < Part<T>::kPer; ++j) {
+                const float x = element<T>(v[i], j);
+                if (x >= bound) {
+                    if (at < kCap) sh.list[at] = key_of(x, p.first(base + i * TH + tid) + j);
+                    ++at;
+                }
             }
         }
-        __syncthreads();
+    };
+    if (__any_sync(kFull, top >= bound)) {
+        if (TH == 32 ? p.size() <= 32 * NV : p.size() <= TH * NV) {
+            append(p.v0);
+        } else {  // every lane goes through its own chunks
+            const int chunks = (p.size() + TH * NV - 1) / (TH * NV);
+            int c = -1;
+            while (true) {
+                do ++c;
+                while (TH > 32 && c < chunks && sh.of_chunk[c % 8][tid] < bound);
+                if (!__any_sync(kFull, c < chunks)) break;
+                const int base = c < chunks ? p.v0 + c * TH * NV : p.v1;  // v1: nothing
+                load_chunk<TH, NV>(p, base, tid, v);
+                append(base);
+            }
+        }
     }
-    const uint32_t bound = sh.bound;
-    auto each_logit = [&](auto&& f) {  // this thread's logits, chunk by chunk
+    group_sync<TH>();
+    return sh.count;
+}
+
+// put(place, key) for the k largest of the list's n keys, and nothing for places past n.
+template <int TH, typename Put>
+__device__ __forceinline__ void order_list(TopShared<TH>& sh, int n, int tid, int k, Put&& put) {
+    if (tid < 8) sh.list[n + tid] = 0;  // a round number to count
+    group_sync<TH>();
+    for (int i = tid; i < n; i += TH) {
+        const Key key = sh.list[i];
+        int place = 0;
+        for (int l = 0; l < n; l += 8)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) place += sh.list[l + q] > key;
+        if (place < k) put(place, key);
+    }
+}
+
+// The k largest of the part without a list: k rounds that each find the largest key below the
+// last one; returns how many there are (one thread puts them).
+template <int TH, int NV, typename T, typename Put>
+__device__ __noinline__ int take_rounds(TopShared<TH>& sh, const Part<T> p, int tid, int k,
+                                        Put put) {
+    Key last = ~Key(0);
+    for (int q = 0; q < k; ++q) {
+        Key best = 0;
         for (int base = p.v0; base < p.v1; base += TH * NV) {
-            if (!one) load_chunk<TH, NV>(p, base, tid, v);
+            uint32_t v[NV][4];
+            load_chunk<TH, NV>(p, base, tid, v);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < Part<T>::kPer; ++j)
-                    f(element<T>(v[i], j), p.first(base + i * TH + tid) + j);
-        }
-    };
-    if (mine >= bound)
-        each_logit([&](float x, int id) {
-            if (order_of(x) >= bound) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kCap) sh.list[at] = key_of(x, id);
-            }
-        });
-    group_sync<TH>();
-    const int n = sh.count;
-    if (n <= kCap) {
-        for (int i = tid; i < n; i += TH) {
-            const Key key = sh.list[i];
-            int place = 0;
-            for (int l = 0; l < n; ++l) place += sh.list[l] > key;
-            if (place < k) put(place, key);
-        }
-        for (int i = n + tid; i < k; i += TH) put(i, Key(0));
-    } else {
-        Key last = ~Key(0);
-        for (int q = 0; q < k; ++q) {
-            Key best = 0;
-            if (last != 0)
-                each_logit([&](float x, int id) {
-                    const Key key = key_of(x, id);
+                for (int j = 0; j < Part<T>::kPer; ++j) {
+                    const float x = element<T>(v[i], j);
+                    const Key key = key_of(x, p.first(base + i * TH + tid) + j);
                     if (x > -kInf && key < last && key > best) best = key;
-                });
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const Key other = __shfl_xor_sync(kFull, best, o);
-                best = other > best ? other : best;
-            }
-            if constexpr (TH > 32) {
-                if (lane == 0) sh.last[tid / 32] = best;
-                __syncthreads();
-                for (int w = 0; w < TH / 32; ++w) best = sh.last[w] > best ? sh.last[w] : best;
-                __syncthreads();
-            }
-            if (tid == 0) put(q, best);
-            last = best;
+                }
         }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const Key other = __shfl_xor_sync(kFull, best, o);
+            best = other > best ? other : best;
+        }
+        if constexpr (TH > 32) {
+            if ((tid & 31) == 0) sh.last[tid / 32] = best;
+            __syncthreads();
+            for (int w = 0; w < TH / 32; ++w) best = sh.last[w] > best ? sh.last[w] : best;
+            __syncthreads();
+        }
+        if (best == 0) return q;
+        if (tid == 0) put(q, best);
+        last = best;
     }
+    return k;
 }
 
 // ------------------------------------------------------------------ forward
 
 template <typename T, int TH, bool kTop>
-__global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob(RowsIn in, TokensIn tk, ValuesOut o) {
+__global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
+    k_logprob(RowsIn in, TokensIn tk, ValuesOut o) {
     constexpr int NV = vectors_of<T, TH>(), kRows = block_of<TH>() / TH;
     __shared__ Joint<TH> joint[kRows];
     __shared__ TopShared<kTop ? TH : 32> tops[kTop ? kRows : 1];
@@ -220,13 +281,14 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob(
     const int tid = TH == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int group = TH == 32 ? threadIdx.x / 32 : 0;
     const int rank = in.cluster > 1 ? (int)cluster_ctarank() : 0;
-    const float c2 = in.c * kLog2e, low = far_below(in.c);
-    int parity = 0;
-    if (in.cluster > 1) cluster_sync();  // every CTA runs before one writes to another
-    for (int64_t r = (int64_t)(blockIdx.x / in.cluster) * kRows + group; r < in.rows;
-         r += (int64_t)(gridDim.x / in.cluster) * kRows) {
-        const int64_t s = r / in.n;
-        const int j = (int)(r - s * in.n);
+    const float c2 = in.c * kLog2e;
+    const int64_t step = (int64_t)(gridDim.x / in.cluster) * kRows;
+    if (in.cluster > 1) cluster_arrive();  // every CTA runs before one writes to another
+    bool started = in.cluster == 1;
+    for (int64_t r = (int64_t)(blockIdx.x / in.cluster) * kRows + group; r < in.rows; r += step) {
+        int64_t s;
+        int j;
+        split_row(r, in.n, s, j);
         const Part<T> p(static_cast<const T*>(in.x) + s * in.ss + j * in.sn, in.V, rank, in.cluster);
         uint32_t v[NV][4];
         load_chunk<TH, NV>(p, p.v0, tid, v);
@@ -240,60 +302,76 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob(
         float top = -kInf;
         for (int base = p.v0; base < p.v1; base += TH * NV) {
             if (base != p.v0) load_chunk<TH, NV>(p, base, tid, v);
-            add_chunk<TH, NV, true, T>(v, p.v1 - base, tid, c2, low, st, top);
-        }
-        st = join_row<TH, true>(joint[group], st, tid, in.cluster, rank, parity, c2, low);
-        parity ^= 1;
-        if (tid == 0 && rank == 0) put_values(o, r, t, xt, in.c, st);
-        if constexpr (kTop) {
-            const bool broken = !(st.s < kInf);
-            const float ln_s = logf(st.s);
-            auto out = [&](int place, Key key) {
-                if (o.top_ids != nullptr) o.top_ids[r * o.k + place] = key ? key_id(key) : -1;
-                if (o.top_logprob != nullptr)
-                    o.top_logprob[r * o.k + place] =
-                        broken ? NAN : key ? log_prob(key_value(key), in.c, st.m, ln_s) : -kInf;
-            };
-            if (broken) {
-                if (rank == 0)
-                    for (int i = tid; i < o.k; i += TH) out(i, Key(0));
-            } else if (TH == 32 || in.cluster == 1) {
-                part_top<TH, NV>(tops[group], p, v, top, tid, o.k, out);
-            } else {
-                const uint32_t to = cluster_map(smem_u32(&lists.of[rank][0]), 0);
-                part_top<TH, NV>(tops[group], p, v, top, tid, o.k,
-                                 [&](int place, Key key) { st_cluster_u64(to + 8 * place, key); });
-                cluster_sync();
-                // a key's place: its own list's, and what the other lists hold above it
-                if (rank == 0)
-                    for (int i = tid; i < in.cluster * o.k; i += TH) {
-                        const int own = i / o.k;
-                        const Key key = lists.of[own][i - own * o.k];
-                        int place = i - own * o.k;
-                        if (key == 0) {  // empty places: behind all keys, in their own order
-                            for (int l = 0; l < in.cluster; ++l) {
-                                if (l == own) continue;
-                                for (int q = 0; q < o.k; ++q)
-                                    place += lists.of[l][q] != 0 || l < own;
-                            }
-                        } else {
-                            for (int l = 0; l < in.cluster; ++l) {
-                                if (l == own) continue;
-                                int a = 0, b = o.k;
-                                while (a < b) {
-                                    const int mid = (a + b) / 2;
-                                    if (lists.of[l][mid] > key) a = mid + 1;
-                                    else b = mid;
-                                }
-                                place += a;
-                            }
-                        }
-                        if (place < o.k) out(place, key);
-                    }
+            const float mx = add_chunk<TH, NV, true, T>(v, p.v1 - base, tid, c2, st);
+            if constexpr (kTop) {
+                top = fmaxf(top, mx);
+                if (TH > 32 && p.size() > TH * NV) {
+                    const int q = (base - p.v0) / (TH * NV);
+                    float& of = tops[group].of_chunk[q % 8][tid];
+                    of = q < 8 ? mx : fmaxf(of, mx);
+                }
             }
         }
-        group_sync<TH>();
+        if constexpr (kTop) leave_maxima<TH>(tops[group], top, tid);
+        st = join_group<TH, true>(joint[group], st, tid, c2);
+        int n = 0;
+        if constexpr (kTop) n = collect<TH, NV>(tops[group], p, v, top, tid, o.k);
+        if (TH > 32 && in.cluster > 1) {  // the first CTA gets the others' triples and keys
+            if (!started) cluster_wait();
+            started = true;
+            if (tid == 0) push_stats<TH, true>(joint[0], st, rank, 0, 0);
+            if constexpr (kTop) {
+                const uint32_t to = cluster_map(smem_u32(&lists.of[rank][0]), 0);
+                auto give = [to](int place, Key key) { st_cluster_u64(to + 8 * place, key); };
+                if (n > TopShared<TH>::kCap) {
+                    n = take_rounds<TH, NV>(tops[0], p, tid, o.k, give);
+                } else if (n > kMaxTop) {
+                    order_list(tops[0], n, tid, o.k, give);
+                    n = o.k;
+                } else {
+                    for (int i = tid; i < n; i += TH) give(i, tops[0].list[i]);
+                }
+                if (tid == 0) st_cluster_u32(cluster_map(smem_u32(&lists.count[rank]), 0), n);
+            }
+            cluster_sync();
+            if (rank == 0) st = join_cluster<TH, true>(joint[0], tid, in.cluster, 0, c2);
+        }
+        if (rank == 0) {
+            if (tid == 0) put_values(o, r, t, xt, in.c, st);
+            if constexpr (kTop) {
+                const bool broken = !(st.s < kInf);
+                const float ln_s = logf(st.s);
+                const int64_t at = r * o.k;
+                auto out = [=](int place, Key key) {
+                    if (o.top_ids != nullptr) o.top_ids[at + place] = key ? key_id(key) : -1;
+                    if (o.top_logprob != nullptr)
+                        o.top_logprob[at + place] =
+                            broken ? NAN : key ? log_prob(key_value(key), in.c, st.m, ln_s) : -kInf;
+                };
+                if (broken) {
+                    n = 0;
+                } else if (in.cluster == 1) {
+                    if (n > TopShared<TH>::kCap) n = take_rounds<TH, NV>(tops[group], p, tid, o.k, out);
+                    else order_list(tops[group], n, tid, o.k, out);
+                } else {
+                    n = 0;
+                    for (int l = 0; l < in.cluster; ++l) {
+                        for (int e = tid; e < lists.count[l]; e += TH)
+                            tops[0].list[n + e] = lists.of[l][e];
+                        n += lists.count[l];
+                    }
+                    order_list(tops[0], n, tid, o.k, out);
+                }
+                for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
+            }
+        }
+        if (TH > 32 && in.cluster > 1) {
+            if (r + step < in.rows) cluster_sync();  // the lists are free again
+        } else {
+            group_sync<TH>();
+        }
     }
+    if (!started) cluster_wait();
 }
 
 // ------------------------------------------------------------------ gradient
@@ -306,14 +384,15 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob_
     const int tid = TH == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int group = TH == 32 ? threadIdx.x / 32 : 0;
     const int rank = in.cluster > 1 ? (int)cluster_ctarank() : 0;
-    const float c2 = in.c * kLog2e, low = far_below(in.c);
+    const float c2 = in.c * kLog2e;
     const bool values = o.logprob != nullptr || o.entropy != nullptr || o.lse != nullptr;
     int parity = 0;
     if (in.cluster > 1) cluster_sync();
     for (int64_t r = (int64_t)(blockIdx.x / in.cluster) * kRows + group; r < in.rows;
          r += (int64_t)(gridDim.x / in.cluster) * kRows) {
-        const int64_t s = r / in.n;
-        const int j = (int)(r - s * in.n);
+        int64_t s;
+        int j;
+        split_row(r, in.n, s, j);
         const Part<T> p(static_cast<const T*>(in.x) + s * in.ss + j * in.sn, in.V, rank, in.cluster);
         // the gradient's row has its own alignment
         T* d = static_cast<T*>(g.d) + s * g.ss + j * g.sn;
@@ -330,21 +409,22 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob_
         if (!zero || values) {
             load_chunk<TH, NV>(p, p.v0, tid, v);
             if (t >= 0 && (owner || (tid == 0 && rank == 0))) xt = widen(p.x[t]);
-            float top = -kInf;
             for (int base = p.v0; base < p.v1; base += TH * NV) {
                 if (base != p.v0) load_chunk<TH, NV>(p, base, tid, v);
-                add_chunk<TH, NV, true, T>(v, p.v1 - base, tid, c2, low, st, top);
+                add_chunk<TH, NV, true, T>(v, p.v1 - base, tid, c2, st);
             }
-            st = join_row<TH, true>(joint[group], st, tid, in.cluster, rank, parity, c2, low);
+            st = join_row<TH, true>(joint[group], st, tid, in.cluster, rank, parity, c2);
             parity ^= 1;
             if (tid == 0 && rank == 0) put_values(o, r, t, xt, in.c, st);
         }
         const bool none = zero || st.s == 0.f;
-        const float m = none ? 0.f : st.m;
         const float inv = none ? 0.f : 1.f / st.s, ln_s = none ? 0.f : logf(st.s);
-        const float h = ln_s - in.c * (st.w * inv);
-        // c p_i [(z - a) - b (ln p_i + H)] = e^{c (x - m)} (c0 + c1 (x - m))
-        const float c0 = in.c * inv * ((z - a) - b * (h - ln_s)), c1 = -in.c * inv * b * in.c;
+        const float h = ln_s - kLn2 * (st.w * inv);
+        // c p_i [(z - a) - b (ln p_i + H)] = 2^t (c0 + c1 t), t = log2(e) c (x - m)
+        const float c0 = in.c * inv * ((z - a) - b * (h - ln_s)), c1 = -in.c * inv * b * kLn2;
+        const Scale k(c2, st.m);
+        const float back = ex2(-k.shift);  // the same for t that are off by the shift
+        const float k0 = back * fmaf(-k.shift, c1, c0), k1 = back * c1;
         for (int base = p.v0; base < p.v1; base += TH * NV) {
             if (!none && p.size() > TH * NV) load_chunk<TH, NV>(p, base, tid, v);
             each_vector<TH, NV>(v, p.v1 - base, tid, [&](int i, uint32_t (&w)[4]) {
@@ -354,17 +434,19 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob_
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) y[e] = 0.f;
                 } else {
-                    add_to(w, -m, y);
+                    Pair q[kPer / 2];
+                    exponents<T, true>(w, k, q);
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e)
-                        y[e] = ex2(y[e] * c2) * fmaf(c1, fmaxf(y[e], low), c0);
+                    for (int e = 0; e < kPer / 2; ++e)
+                        halves(mul2(ex2_pair(q[e]), fma2(pair_of(k1, k1), q[e], pair_of(k0, k0))),
+                               y[2 * e], y[2 * e + 1]);
                 }
                 store_vector<T>(d, at, y, wide && vec >= p.lo && vec < p.hi, vec < p.v1, in.V);
             });
         }
         if (owner && !none) {
-            const float df = xt - m;
-            narrow(ex2(df * c2) * fmaf(c1, fmaxf(df, low), c0) + in.c * a, d + t);
+            const float e = exponent(xt, st.m, c2);
+            narrow(fmaf(ex2(e), fmaf(c1, e, c0), in.c * a), d + t);
         }
         group_sync<TH>();
     }
@@ -376,8 +458,7 @@ cudaError_t forward_of(const Shape& sh, const RowsIn& in, const TokensIn& tk, co
     switch (sh.threads) {
         case 32: return launch_rows(k_logprob<T, 32, kTop>, 32, in, 0, s, in, tk, o);
         case 128: return launch_rows(k_logprob<T, 128, kTop>, 128, in, 0, s, in, tk, o);
-        case 256: return launch_rows(k_logprob<T, 256, kTop>, 256, in, 0, s, in, tk, o);
-        default: return launch_rows(k_logprob<T, 512, kTop>, 512, in, 0, s, in, tk, o);
+        default: return launch_rows(k_logprob<T, 256, kTop>, 256, in, 0, s, in, tk, o);
     }
 }
 
@@ -416,7 +497,7 @@ extern "C" int mimi_rvq_token_logprob(const void* logits, int dtype, int64_t S, 
     if (top_k > 0 && (!maybe_on_device(top_ids, 4, dev) || !maybe_on_device(top_logprob, 4, dev)))
         return MIMI_RVQ_EINVAL;
     const int k = top_ids != nullptr || top_logprob != nullptr ? top_k : 0;
-    const Shape sh = shape_of(S * n, V, size, k <= kWarpTop);
+    const Shape sh = shape_of(S * n, V, size, k <= kWarpTop, false);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.cluster};
     const TokensIn tk{tokens, tok_stride_s, tok_stride_n, pad,
                       reinterpret_cast<unsigned long long*>(n_bad)};
@@ -451,7 +532,7 @@ extern "C" int mimi_rvq_token_logprob_grad(
         !maybe_on_device(logprob, 4, dev) || !maybe_on_device(entropy, 4, dev) ||
         !maybe_on_device(lse, 4, dev) || !maybe_on_device(n_bad, 8, dev))
         return MIMI_RVQ_EINVAL;
-    const Shape sh = shape_of(S * n, V, size, true);
+    const Shape sh = shape_of(S * n, V, size, true, true);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.cluster};
     const TokensIn tk{tokens, tok_stride_s, tok_stride_n, pad,
                       reinterpret_cast<unsigned long long*>(n_bad)};
