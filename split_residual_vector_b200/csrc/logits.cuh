@@ -193,6 +193,18 @@ __device__ __forceinline__ float exponent(float x, float m, float c2) {
     return max_nan((x - (m == -kInf ? 0.f : m)) * c2, kLow);
 }
 
+// ln of a sum (0: -inf); the approximate logarithm is within 2^-22.
+__device__ __forceinline__ float ln(float s) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r * kLn2;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // ln p of a logit of the row. Logits of opposite sign near float32's limits, whose difference or
 // product overflows, are taken in float64.
 __device__ __forceinline__ float log_prob(float x, float c, float m, float ln_s) {
@@ -203,11 +215,28 @@ __device__ __forceinline__ float log_prob(float x, float c, float m, float ln_s)
 
 // ------------------------------------------------------------------ rows
 
-// Step and stream of a row.
-__device__ __forceinline__ void split_row(int64_t r, int n, int64_t& s, int& j) {
-    s = n == 1 ? r : (r >> 32) == 0 ? (int64_t)((uint32_t)r / (uint32_t)n) : r / n;
-    j = (int)(r - s * n);
-}
+// The rows r, r + step, ... of a group, as step s and stream j.
+struct RowWalk {
+    int64_t r, s, step, ds;
+    int j, dj;
+    __device__ __forceinline__ RowWalk(int64_t first, int64_t step_, int n) : r(first), step(step_) {
+        split(r, n, s, j);
+        split(step, n, ds, dj);
+    }
+    __device__ __forceinline__ static void split(int64_t v, int n, int64_t& q, int& rem) {
+        q = n == 1 ? v : (v >> 32) == 0 ? (int64_t)((uint32_t)v / (uint32_t)n) : v / n;
+        rem = (int)(v - q * n);
+    }
+    __device__ __forceinline__ void next(int n) {
+        r += step;
+        s += ds;
+        j += dj;
+        if (j >= n) {
+            j -= n;
+            ++s;
+        }
+    }
+};
 
 // One thread group's share of a row: vectors [v0, v1), of which [lo, hi) lie wholly in the row.
 template <typename T>
@@ -314,11 +343,31 @@ __device__ __forceinline__ void put_edge(const Part<T>& p, int vec, int base, in
     }
 }
 
+// The slots i < NV of a chunk in which a warp has vectors (base + i * TH + tid), and whether all
+// of its vectors in the chunk lie wholly in the row (the same for a warp's lanes).
+template <int TH, int NV, typename T>
+struct Slots {
+    int count;
+    bool whole;
+    __device__ __forceinline__ Slots(const Part<T>& p, int base, int tid) {
+        const int first = base + (tid & ~31);
+        if constexpr (TH == 32) count = min((p.v1 - first + 31) / 32, NV);
+        else count = min((p.v1 - first + TH - 1) / TH, NV);
+        whole = count == NV && first >= p.lo && first + (NV - 1) * TH + 32 <= p.hi;
+    }
+};
+
 // A chunk's vectors: base + i * TH + tid, i < NV; -inf past the part's end.
 template <int TH, int NV, typename T>
 __device__ __forceinline__ void load_chunk(const Part<T>& p, int base, int tid,
                                            uint32_t (&v)[NV][4]) {
     const T* at = p.x + p.first(base + tid);
+    const Slots<TH, NV, T> sl(p, base, tid);
+    if (sl.whole) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) load16(at + i * TH * Elem<T>::kPer, v[i]);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int vec = base + i * TH + tid;
@@ -355,13 +404,31 @@ __device__ __forceinline__ void hide(const uint8_t* mark, uint32_t (&v)[NV][4]) 
     }
 }
 
-// f(vector of the chunk, its registers) for this thread's vectors below `here`, the number of
-// vectors from the chunk's base to the part's end; whole warps past it skip.
-template <int TH, int NV, typename F>
-__device__ __forceinline__ void each_vector(uint32_t (&v)[NV][4], int here, int tid, F&& f) {
+// f(i, registers) for the warp's slots.
+template <int NV, typename F>
+__device__ __forceinline__ void each_slot(uint32_t (&v)[NV][4], int count, F&& f) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (i * TH + (tid & ~31) < here) f(i, v[i]);
+    for (int i = 0; i < NV; ++i) {
+        if (i >= count) break;
+        f(i, v[i]);
+    }
+}
+
+// Stores the gradients make(registers, y) of a chunk into the row d.
+template <int TH, int NV, typename T, typename F>
+__device__ __forceinline__ void store_chunk(const Part<T>& p, int base, int tid, T* d, bool wide,
+                                            uint32_t (&v)[NV][4], F&& make) {
+    constexpr int kPer = Elem<T>::kPer;
+    const Slots<TH, NV, T> sl(p, base, tid);
+    const int at = p.first(base + tid);
+    const bool whole = sl.whole && wide;
+    each_slot<NV>(v, sl.count, [&](int i, uint32_t (&w)[4]) {
+        const int vec = base + i * TH + tid;
+        float y[kPer];
+        make(w, y);
+        store_vector<T>(d, at + i * TH * kPer, y, whole || (wide && vec >= p.lo && vec < p.hi),
+                        vec < p.v1, p.V);
+    });
 }
 
 template <typename T>
@@ -382,18 +449,19 @@ struct Stats {
 // Adds a chunk to a warp's running statistics: m is the warp's, s and w are the thread's.
 // Returns the thread's own maximum in the chunk.
 template <int TH, int NV, bool kW, typename T>
-__device__ __forceinline__ float add_chunk(uint32_t (&v)[NV][4], int here, int tid, float c2,
-                                           Stats& st) {
+__device__ __forceinline__ float add_chunk(const Part<T>& p, int base, int tid,
+                                           uint32_t (&v)[NV][4], float c2, Stats& st) {
+    const int count = Slots<TH, NV, T>(p, base, tid).count;
     float mx;
     if constexpr (sizeof(T) == 4) {
         mx = -kInf;
-        each_vector<TH, NV>(v, here, tid, [&](int, uint32_t (&w)[4]) {
+        each_slot<NV>(v, count, [&](int, uint32_t (&w)[4]) {
             mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]))),
                        fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
         });
     } else {
         uint32_t a = Elem<T>::kFill;
-        each_vector<TH, NV>(v, here, tid, [&](int, uint32_t (&w)[4]) {
+        each_slot<NV>(v, count, [&](int, uint32_t (&w)[4]) {
             a = max_bf16x2(max_bf16x2(a, max_bf16x2(w[0], w[1])), max_bf16x2(w[2], w[3]));
         });
         mx = fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a));
@@ -407,7 +475,7 @@ __device__ __forceinline__ float add_chunk(uint32_t (&v)[NV][4], int here, int t
     }
     st.m = m;
     Pair s2 = 0, w2 = 0;  // (0, 0)
-    each_vector<TH, NV>(v, here, tid, [&](int, uint32_t (&w)[4]) {
+    each_slot<NV>(v, count, [&](int, uint32_t (&w)[4]) {
         Pair t[Elem<T>::kPer / 2];
         exponents<T, kW>(w, k, t);
 #pragma unroll

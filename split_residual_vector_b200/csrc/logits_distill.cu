@@ -71,11 +71,11 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
     ListShared& ls = lists[group];
     int parity = 0;
     if (in.cluster > 1) cluster_sync();
-    for (int64_t r = (int64_t)(blockIdx.x / in.cluster) * kRows + group; r < in.rows;
-         r += (int64_t)(gridDim.x / in.cluster) * kRows) {
-        int64_t s;
-        int j;
-        split_row(r, in.n, s, j);
+    RowWalk at_row((int64_t)(blockIdx.x / in.cluster) * kRows + group,
+                   (int64_t)(gridDim.x / in.cluster) * kRows, in.n);
+    for (; at_row.r < in.rows; at_row.next(in.n)) {
+        const int64_t r = at_row.r, s = at_row.s;
+        const int j = at_row.j;
         const Part<T> p(static_cast<const T*>(in.x) + s * in.ss + j * in.sn, in.V, rank, in.cluster);
         const int chunks = (p.size() + TH * NV - 1) / (TH * NV);
         uint8_t* mark = marks + (size_t)group * most_chunks<T, TH>(in.V, in.cluster) * TH * NV;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
                 const int base = p.v0 + q2 * TH * NV;
                 if (q2) load_chunk<TH, NV>(p, base, tid, v);
                 hide<NV, T>(mark + (q2 * TH + tid) * NV, v);
-                add_chunk<TH, NV, false, T>(v, p.v1 - base, tid, c2, rest);
+                add_chunk<TH, NV, false, T>(p, base, tid, v, c2, rest);
             }
             if (in.cluster > 1 && tid < in.cluster) {
                 const uint32_t to = cluster_map(smem_u32(&listed_of.cta[parity][0][rank]), tid);
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
         const float qr = rest.s == 0.f ? 0.f : ls.tail_q;
         const float Q = te.tail ? ls.Q + qr : ls.Q;
         if (te.loss != nullptr && rank == 0 && tid < 32) {
-            const float ln_s = logf(all.s);
+            const float ln_s = ln(all.s);
             float part = 0.f;
             if (!empty) {
                 for (int e = tid; e < te.k; e += 32)
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
                         part += ls.q[e] * (ls.lq[e] - (all.s == 0.f ? -kInf : log_prob(ls.x[e], in.c, all.m, ln_s)));
                 part = warp_sum(part);
                 if (qr > 0.f)
-                    part += qr * (logf(qr) - (in.c * (rest.m - all.m) + logf(rest.s) - ln_s));
+                    part += qr * (logf(qr) - (in.c * (rest.m - all.m) + ln(rest.s) - ln_s));
             }
             if (tid == 0) te.loss[r] = part;
         }
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
             T* d = static_cast<T*>(te.d) + s * te.d_ss + j * te.d_sn;
             const bool wide =
                 ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(p.x)) & 15u) == 0;
-            const float gc = g * in.c, inv = none ? 0.f : 1.f / all.s;
+            const float gc = g * in.c, inv = none ? 0.f : reciprocal(all.s);
             const Scale k(c2, rest.m);
             // a rest of -inf only has no gradient of its own: 2^t is 0 there
             const float f = none ? 0.f
@@ -252,9 +252,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
                     load_chunk<TH, NV>(p, base, tid, v);
                     hide<NV, T>(mark + (q2 * TH + tid) * NV, v);
                 }
-                each_vector<TH, NV>(v, p.v1 - base, tid, [&](int i, uint32_t (&w)[4]) {
-                    const int vec = base + i * TH + tid, at = p.first(vec);
-                    float y[kPer];
+                store_chunk<TH, NV>(p, base, tid, d, wide, v, [&](const uint32_t (&w)[4], float (&y)[kPer]) {
                     if (none) {
 #pragma unroll
                         for (int e = 0; e < kPer; ++e) y[e] = 0.f;
@@ -265,7 +263,6 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_distill(
                         for (int e = 0; e < kPer / 2; ++e)
                             halves(mul2(ex2_pair(t[e]), pair_of(f, f)), y[2 * e], y[2 * e + 1]);
                     }
-                    store_vector<T>(d, at, y, wide && vec >= p.lo && vec < p.hi, vec < p.v1, in.V);
                 });
             }
             group_sync<TH>();  // the listed tokens' places hold the rest's gradient by now

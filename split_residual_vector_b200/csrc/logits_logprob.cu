@@ -80,11 +80,11 @@ __device__ __forceinline__ int target_of(const TokensIn& tk, int64_t s, int j, i
 
 __device__ __forceinline__ void put_values(const ValuesOut& o, int64_t r, int t, float xt, float c,
                                            const Stats& st) {
-    const float ln_s = logf(st.s);
+    const float ln_s = ln(st.s);
     const bool none = st.s == 0.f;
     if (o.logprob != nullptr)
         o.logprob[r] = t < 0 ? 0.f : none ? -kInf : log_prob(xt, c, st.m, ln_s);
-    if (o.entropy != nullptr) o.entropy[r] = none ? 0.f : ln_s - kLn2 * (st.w / st.s);
+    if (o.entropy != nullptr) o.entropy[r] = none ? 0.f : ln_s - kLn2 * (st.w * reciprocal(st.s));
     if (o.lse != nullptr) o.lse[r] = none ? -kInf : c * st.m + ln_s;
 }
 
@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
     const int64_t step = (int64_t)(gridDim.x / in.cluster) * kRows;
     if (in.cluster > 1) cluster_arrive();  // every CTA runs before one writes to another
     bool started = in.cluster == 1;
-    for (int64_t r = (int64_t)(blockIdx.x / in.cluster) * kRows + group; r < in.rows; r += step) {
-        int64_t s;
-        int j;
-        split_row(r, in.n, s, j);
+    RowWalk at_row((int64_t)(blockIdx.x / in.cluster) * kRows + group, step, in.n);
+    for (; at_row.r < in.rows; at_row.next(in.n)) {
+        const int64_t r = at_row.r, s = at_row.s;
+        const int j = at_row.j;
         const Part<T> p(static_cast<const T*>(in.x) + s * in.ss + j * in.sn, in.V, rank, in.cluster);
         uint32_t v[NV][4];
         load_chunk<TH, NV>(p, p.v0, tid, v);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
         float top = -kInf;
         for (int base = p.v0; base < p.v1; base += TH * NV) {
             if (base != p.v0) load_chunk<TH, NV>(p, base, tid, v);
-            const float mx = add_chunk<TH, NV, true, T>(v, p.v1 - base, tid, c2, st);
+            const float mx = add_chunk<TH, NV, true, T>(p, base, tid, v, c2, st);
             if constexpr (kTop) {
                 top = fmaxf(top, mx);
                 if (TH > 32 && p.size() > TH * NV) {
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
             if (tid == 0) put_values(o, r, t, xt, in.c, st);
             if constexpr (kTop) {
                 const bool broken = !(st.s < kInf);
-                const float ln_s = logf(st.s);
+                const float ln_s = ln(st.s);
                 const int64_t at = r * o.k;
                 auto out = [=](int place, Key key) {
                     if (o.top_ids != nullptr) o.top_ids[at + place] = key ? key_id(key) : -1;
@@ -388,11 +388,11 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob_
     const bool values = o.logprob != nullptr || o.entropy != nullptr || o.lse != nullptr;
     int parity = 0;
     if (in.cluster > 1) cluster_sync();
-    for (int64_t r = (int64_t)(blockIdx.x / in.cluster) * kRows + group; r < in.rows;
-         r += (int64_t)(gridDim.x / in.cluster) * kRows) {
-        int64_t s;
-        int j;
-        split_row(r, in.n, s, j);
+    RowWalk at_row((int64_t)(blockIdx.x / in.cluster) * kRows + group,
+                   (int64_t)(gridDim.x / in.cluster) * kRows, in.n);
+    for (; at_row.r < in.rows; at_row.next(in.n)) {
+        const int64_t r = at_row.r, s = at_row.s;
+        const int j = at_row.j;
         const Part<T> p(static_cast<const T*>(in.x) + s * in.ss + j * in.sn, in.V, rank, in.cluster);
         // the gradient's row has its own alignment
         T* d = static_cast<T*>(g.d) + s * g.ss + j * g.sn;
@@ -411,14 +411,14 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob_
             if (t >= 0 && (owner || (tid == 0 && rank == 0))) xt = widen(p.x[t]);
             for (int base = p.v0; base < p.v1; base += TH * NV) {
                 if (base != p.v0) load_chunk<TH, NV>(p, base, tid, v);
-                add_chunk<TH, NV, true, T>(v, p.v1 - base, tid, c2, st);
+                add_chunk<TH, NV, true, T>(p, base, tid, v, c2, st);
             }
             st = join_row<TH, true>(joint[group], st, tid, in.cluster, rank, parity, c2);
             parity ^= 1;
             if (tid == 0 && rank == 0) put_values(o, r, t, xt, in.c, st);
         }
         const bool none = zero || st.s == 0.f;
-        const float inv = none ? 0.f : 1.f / st.s, ln_s = none ? 0.f : logf(st.s);
+        const float inv = none ? 0.f : reciprocal(st.s), ln_s = none ? 0.f : ln(st.s);
         const float h = ln_s - kLn2 * (st.w * inv);
         // c p_i [(z - a) - b (ln p_i + H)] = 2^t (c0 + c1 t), t = log2(e) c (x - m)
         const float c0 = in.c * inv * ((z - a) - b * (h - ln_s)), c1 = -in.c * inv * b * kLn2;
@@ -427,9 +427,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob_
         const float k0 = back * fmaf(-k.shift, c1, c0), k1 = back * c1;
         for (int base = p.v0; base < p.v1; base += TH * NV) {
             if (!none && p.size() > TH * NV) load_chunk<TH, NV>(p, base, tid, v);
-            each_vector<TH, NV>(v, p.v1 - base, tid, [&](int i, uint32_t (&w)[4]) {
-                const int vec = base + i * TH + tid, at = p.first(vec);
-                float y[kPer];
+            store_chunk<TH, NV>(p, base, tid, d, wide, v, [&](const uint32_t (&w)[4], float (&y)[kPer]) {
                 if (none) {
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) y[e] = 0.f;
@@ -441,7 +439,6 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob_
                         halves(mul2(ex2_pair(q[e]), fma2(pair_of(k1, k1), q[e], pair_of(k0, k0))),
                                y[2 * e], y[2 * e + 1]);
                 }
-                store_vector<T>(d, at, y, wide && vec >= p.lo && vec < p.hi, vec < p.v1, in.V);
             });
         }
         if (owner && !none) {
