@@ -48,7 +48,7 @@ extern "C" {
 #define MIMI_RVQ_AUDIO_PAD 2048   /* pad id of an audio stream */
 #define MIMI_RVQ_MAX_STREAMS 64   /* largest K for mimi_rvq_embed_sum */
 #define MIMI_RVQ_MAX_TOP 128      /* largest top_k / teacher list of the logits calls */
-#define MIMI_RVQ_MAX_VOCAB (1 << 20) /* largest V of the logits calls */
+#define MIMI_RVQ_MAX_VOCAB (3 << 17) /* largest V of the logits calls: 393216 */
 
 /*
  * Pack T frames into the multi-stream sequence packed [S][K], K = 1 + 8 *

@@ -28,7 +28,7 @@ EXPORTS = ("mimi_rvq_create", "mimi_rvq_destroy", "mimi_rvq_encode", "mimi_rvq_e
            "mimi_rvq_encode_noalloc", "mimi_rvq_streams_get_error",
            "mimi_rvq_streams_wait_selftest", "mimi_rvq_token_logprob",
            "mimi_rvq_token_logprob_grad", "mimi_rvq_distill_topk", "mimi_rvq_distill_topk_grad")
-MAX_TOP, MAX_VOCAB = 128, 1 << 20
+MAX_TOP, MAX_VOCAB = 128, 3 << 17
 TEXT_CARD, TEXT_PAD, AUDIO_PAD = 32000, 32000, 2048
 
 _lib = None

@@ -1,20 +1,23 @@
 // logits.cuh -- what the kernels on the language model's logits share: a row's
-// layout, its loads, the pass that gives its softmax statistics, and the host
-// side's choice of threads.
+// layout, its way into shared memory, the passes that give its softmax
+// statistics, and the host side's choice of threads.
 //
-// A row is one position of one stream: V logits that start at any element. It
-// is cut into 16-byte vectors on aligned addresses (the first and the last may
-// be partly outside the row: their outside elements read as -inf and are never
-// stored), and thread t of the TH that share a row takes vectors t, t + TH, ...
-// Up to NV vectors per thread are kept in registers, so a gradient reads its
-// row once; a longer part is walked in chunks of TH * NV vectors.
+// A row is one position of one stream: V logits that start at any element. Its
+// whole 16-byte vectors (on aligned addresses) are copied into shared memory
+// asynchronously, thread t of the TH that share the row taking vectors t, t + TH,
+// ...; each thread works only on vectors that it copied, so a row needs no
+// barrier before its passes. The up to 2 x 7 elements before the first and after
+// the last whole vector are taken as single values by 16 lanes of the first warp.
+// A group (a warp for short rows, else a CTA, or a cluster of them that splits a
+// row's vectors) goes through rows in a loop and sends for the next row as soon
+// as it has read a row for the last time; several groups per SM overlap one's
+// joining and output with the others' copies and passes.
 //
 // Every statistic comes from m = max x, s = sum 2^t_i and w = sum 2^t_i t_i with
 // t_i = log2(e) c (x_i - m), c = scale, all in float32:
 //     lse = c m + ln s,  ln p_i = c (x_i - m) - ln s,  entropy = ln s - ln 2 w / s.
-// Each warp sums against its own maximum (one hardware reduction), so a row
-// needs one barrier, where the warps' triples are joined; a row split over a
-// cluster needs one cluster barrier more.
+// Each warp sums against its own maximum (one hardware reduction); the warps'
+// triples are joined behind one barrier, a cluster's behind one more.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,7 +45,8 @@ struct RowsIn {
     int64_t rows;  // S * n
     int n, V;
     float c;       // scale
-    int cluster;   // CTAs per row (1: a row is one CTA's or one warp's)
+    int log_cluster;  // CTAs per row: 1 << log_cluster (0: a row is one CTA's or one warp's)
+    int slots;     // 16-byte places of a group's buffer
 };
 
 // ------------------------------------------------------------------ elements
@@ -238,197 +242,98 @@ struct RowWalk {
     }
 };
 
-// One thread group's share of a row: vectors [v0, v1), of which [lo, hi) lie wholly in the row.
+// One group's share of a row.
 template <typename T>
 struct Part {
+    static constexpr int kPer = Elem<T>::kPer;
     const T* x;
     int V;
-    int a;  // elements between the 16-byte boundary at or below x and x
-    int v0, v1, lo, hi;
+    int head;    // elements before the row's first whole vector
+    int tail;    // first element after its last one
+    int first;   // first element of this share's vectors
+    int nv;      // vectors of this share
 
-    static constexpr int kPer = Elem<T>::kPer;
-
-    __device__ Part(const T* row, int V_, int rank, int cluster) : x(row), V(V_) {
-        a = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-        const int all = (a + V + kPer - 1) / kPer;
-        const int per = (all + cluster - 1) >> (31 - __clz(cluster));  // a power of two
-        v0 = min(rank * per, all);
-        v1 = min(v0 + per, all);
-        lo = max(v0, a ? 1 : 0);
-        hi = min(v1, (a + V) / kPer);
+    __device__ __forceinline__ Part(const T* row, int V_, int rank, int log_cluster) : x(row), V(V_) {
+        const int a = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+        head = min(V, (kPer - a) & (kPer - 1));
+        const int whole = (V - head) / kPer;
+        tail = head + whole * kPer;
+        const int per = (whole + (1 << log_cluster) - 1) >> log_cluster;
+        const int v0 = min(rank * per, whole);
+        nv = min(per, whole - v0);
+        first = head + v0 * kPer;
     }
-    __device__ int size() const { return v1 - v0; }
-    // element index of a vector's first element (below 0 or past V at the row's ends)
-    __device__ int first(int vec) const { return vec * kPer - a; }
-    // vector and place of an element
-    __device__ int vector_of(int i) const { return (i + a) / kPer; }
-    __device__ bool holds(int vec) const { return vec >= v0 && vec < v1; }
+    // place of element i in the share's buffer, -1 if it has none
+    __device__ __forceinline__ int place(int i) const {
+        const int q = i - first;
+        return q >= 0 && q < nv * kPer ? q : -1;
+    }
+    // element that lane l < 16 of the row's first warp has beside the vectors, -1 for none
+    __device__ __forceinline__ int edge(int l) const {
+        if (l < 8) return l < head ? l : -1;
+        return l < 16 && tail + l - 8 < V ? tail + l - 8 : -1;
+    }
+    // that lane's place for an element beside the vectors
+    __device__ __forceinline__ int edge_lane(int i) const { return i < head ? i : 8 + i - tail; }
+    __device__ __forceinline__ bool in_edges(int i) const { return i < head || i >= tail; }
 };
 
-__device__ __forceinline__ void load16(const void* p, uint32_t (&w)[4]) {
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "l"(p));
+__device__ __forceinline__ void copy16(void* smem, const void* gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem)
+                 : "memory");
 }
+// Sends for the share's vectors; they have come when arrived() returns.
+template <int TH, typename T>
+__device__ __forceinline__ void fetch(uint4* buf, const Part<T>& p, int tid) {
+    const T* src = p.x + p.first;
+#pragma unroll 4
+    for (int i = tid; i < p.nv; i += TH) copy16(buf + i, src + (size_t)i * Elem<T>::kPer);
+}
+__device__ __forceinline__ void arrived() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void store16(void* p, const uint32_t (&w)[4]) {
     asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(w[0]), "r"(w[1]),
                  "r"(w[2]), "r"(w[3])
                  : "memory");
 }
-
-// The vector at a row's end, element by element; -inf outside the row.
+// A vector's gradients, rounded once; element by element where the gradient's row is not aligned
+// as the logits' is.
 template <typename T>
-__device__ __noinline__ uint4 load_edge(const T* x, int first, int V) {
+__device__ __forceinline__ void store_vector(T* at, bool wide, const float (&y)[Elem<T>::kPer]) {
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = Elem<T>::kFill;
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(y[j]);
+        else w[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+    }
+    if (wide) {
+        store16(at, w);
+    } else {
 #pragma unroll
-    for (int j = 0; j < Elem<T>::kPer; ++j) {
-        const int i = first + j;
-        if (i >= 0 && i < V) {
-            if constexpr (sizeof(T) == 4) {
-                w[j] = __float_as_uint(x[i]);
-            } else {
-                const uint32_t b = __bfloat16_as_ushort(x[i]);
-                w[j / 2] = (j & 1) ? ((w[j / 2] & 0xFFFFu) | (b << 16)) : ((w[j / 2] & 0xFFFF0000u) | b);
-            }
+        for (int j = 0; j < Elem<T>::kPer; ++j) narrow(element<T>(w, j), at + j);
+    }
+}
+
+// f(i, vector i of the share) for this thread's vectors, in groups of four.
+template <int TH, typename F>
+__device__ __forceinline__ void each_vector(const uint4* buf, int nv, int tid, F&& f) {
+    int i = tid;
+    for (; i + 3 * TH < nv; i += 4 * TH) {
+        uint4 q[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) q[u] = buf[i + u * TH];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+            f(i + u * TH, w);
         }
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// A vector's gradients, rounded once: whole at an aligned place, or element by element (those of
-// the row) where the row's ends or the gradient's own alignment want it.
-template <typename T>
-__device__ __forceinline__ void store_vector(T* row, int first, const float (&y)[4], bool whole,
-                                             bool some, int V) {
-    if (whole) {
-        const uint32_t w[4] = {__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
-                               __float_as_uint(y[3])};
-        store16(row + first, w);
-    } else if (some) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (first + j >= 0 && first + j < V) narrow(y[j], row + first + j);
+#pragma unroll 1
+    for (; i < nv; i += TH) {
+        const uint4 q = buf[i];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        f(i, w);
     }
-}
-template <typename T>
-__device__ __forceinline__ void store_vector(T* row, int first, const float (&y)[8], bool whole,
-                                             bool some, int V) {
-    if (whole) {
-        const uint32_t w[4] = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                               pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
-        store16(row + first, w);
-    } else if (some) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (first + j >= 0 && first + j < V) narrow(y[j], row + first + j);
-    }
-}
-
-// Loads vector `vec` of the row's ends into its place of the chunk, if it is this thread's.
-template <int TH, int NV, typename T>
-__device__ __forceinline__ void put_edge(const Part<T>& p, int vec, int base, int tid,
-                                         uint32_t (&v)[NV][4]) {
-    const int at = vec - base - tid;
-    if (vec < p.v0 || vec >= p.v1 || at < 0 || at >= NV * TH || at % TH != 0) return;
-    const uint4 w = load_edge(p.x, p.first(vec), p.V);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool here = at == i * TH;
-        v[i][0] = here ? w.x : v[i][0];
-        v[i][1] = here ? w.y : v[i][1];
-        v[i][2] = here ? w.z : v[i][2];
-        v[i][3] = here ? w.w : v[i][3];
-    }
-}
-
-// The slots i < NV of a chunk in which a warp has vectors (base + i * TH + tid), and whether all
-// of its vectors in the chunk lie wholly in the row (the same for a warp's lanes).
-template <int TH, int NV, typename T>
-struct Slots {
-    int count;
-    bool whole;
-    __device__ __forceinline__ Slots(const Part<T>& p, int base, int tid) {
-        const int first = base + (tid & ~31);
-        if constexpr (TH == 32) count = min((p.v1 - first + 31) / 32, NV);
-        else count = min((p.v1 - first + TH - 1) / TH, NV);
-        whole = count == NV && first >= p.lo && first + (NV - 1) * TH + 32 <= p.hi;
-    }
-};
-
-// A chunk's vectors: base + i * TH + tid, i < NV; -inf past the part's end.
-template <int TH, int NV, typename T>
-__device__ __forceinline__ void load_chunk(const Part<T>& p, int base, int tid,
-                                           uint32_t (&v)[NV][4]) {
-    const T* at = p.x + p.first(base + tid);
-    const Slots<TH, NV, T> sl(p, base, tid);
-    if (sl.whole) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) load16(at + i * TH * Elem<T>::kPer, v[i]);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int vec = base + i * TH + tid;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = Elem<T>::kFill;
-        if (vec >= p.lo && vec < p.hi) load16(at + i * TH * Elem<T>::kPer, v[i]);
-    }
-    // the row's ends, where they are not whole vectors (one of them if the row is that short)
-    put_edge<TH, NV>(p, p.lo - 1, base, tid, v);
-    if (p.hi >= p.lo) put_edge<TH, NV>(p, p.hi, base, tid, v);
-}
-
-// Puts -inf in the place of marked elements: mark[i] has a bit per element of vector i.
-template <int NV, typename T>
-__device__ __forceinline__ void hide(const uint8_t* mark, uint32_t (&v)[NV][4]) {
-#pragma unroll
-    for (int h = 0; h < NV / 4; ++h) {
-        const uint32_t four = *reinterpret_cast<const uint32_t*>(mark + 4 * h);
-        if (four == 0) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t b = (four >> (8 * i)) & 0xFFu;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t& w = v[4 * h + i][j];
-                if constexpr (sizeof(T) == 4) {
-                    if ((b >> j) & 1u) w = Elem<T>::kFill;
-                } else {
-                    if ((b >> (2 * j)) & 1u) w = (w & 0xFFFF0000u) | 0xFF80u;
-                    if ((b >> (2 * j)) & 2u) w = (w & 0xFFFFu) | 0xFF800000u;
-                }
-            }
-        }
-    }
-}
-
-// f(i, registers) for the warp's slots.
-template <int NV, typename F>
-__device__ __forceinline__ void each_slot(uint32_t (&v)[NV][4], int count, F&& f) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (i >= count) break;
-        f(i, v[i]);
-    }
-}
-
-// Stores the gradients make(registers, y) of a chunk into the row d.
-template <int TH, int NV, typename T, typename F>
-__device__ __forceinline__ void store_chunk(const Part<T>& p, int base, int tid, T* d, bool wide,
-                                            uint32_t (&v)[NV][4], F&& make) {
-    constexpr int kPer = Elem<T>::kPer;
-    const Slots<TH, NV, T> sl(p, base, tid);
-    const int at = p.first(base + tid);
-    const bool whole = sl.whole && wide;
-    each_slot<NV>(v, sl.count, [&](int i, uint32_t (&w)[4]) {
-        const int vec = base + i * TH + tid;
-        float y[kPer];
-        make(w, y);
-        store_vector<T>(d, at + i * TH * kPer, y, whole || (wide && vec >= p.lo && vec < p.hi),
-                        vec < p.v1, p.V);
-    });
 }
 
 template <typename T>
@@ -446,36 +351,27 @@ struct Stats {
     float m, s, w;  // m is -inf where no logit is above it
 };
 
-// Adds a chunk to a warp's running statistics: m is the warp's, s and w are the thread's.
-// Returns the thread's own maximum in the chunk.
-template <int TH, int NV, bool kW, typename T>
-__device__ __forceinline__ float add_chunk(const Part<T>& p, int base, int tid,
-                                           uint32_t (&v)[NV][4], float c2, Stats& st) {
-    const int count = Slots<TH, NV, T>(p, base, tid).count;
-    float mx;
+// A warp's statistics over its threads' vectors and edge values (-inf for none): m is the warp's,
+// s and w the thread's own. top: the thread's own maximum.
+template <int TH, bool kW, typename T>
+__device__ __forceinline__ Stats pass(const uint4* buf, int nv, int tid, float edge, float c2,
+                                      float& top) {
     if constexpr (sizeof(T) == 4) {
-        mx = -kInf;
-        each_slot<NV>(v, count, [&](int, uint32_t (&w)[4]) {
-            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]))),
-                       fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+        top = edge;
+        each_vector<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
+            top = fmaxf(top, vector_max<T>(w));
         });
     } else {
         uint32_t a = Elem<T>::kFill;
-        each_slot<NV>(v, count, [&](int, uint32_t (&w)[4]) {
-            a = max_bf16x2(max_bf16x2(a, max_bf16x2(w[0], w[1])), max_bf16x2(w[2], w[3]));
+        each_vector<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
+            a = max_bf16x2(a, max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3])));
         });
-        mx = fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a));
+        top = fmaxf(edge, fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a)));
     }
-    const float m = fmaxf(st.m, warp_max(mx));
-    const Scale k(c2, m);
-    if (st.m != m && st.m != -kInf) {  // an earlier chunk's sums move to the new maximum
-        const float t = exponent(st.m, m, c2), f = ex2(t);
-        if constexpr (kW) st.w = f * fmaf(st.s, t, st.w);
-        st.s *= f;
-    }
-    st.m = m;
+    Stats st{warp_max(top), 0.f, 0.f};
+    const Scale k(c2, st.m);
     Pair s2 = 0, w2 = 0;  // (0, 0)
-    each_slot<NV>(v, count, [&](int, uint32_t (&w)[4]) {
+    each_vector<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
         Pair t[Elem<T>::kPer / 2];
         exponents<T, kW>(w, k, t);
 #pragma unroll
@@ -493,9 +389,10 @@ __device__ __forceinline__ float add_chunk(const Part<T>& p, int base, int tid,
         w += w1;
     }
     const float back = ex2(-k.shift);
-    st.s = fmaf(s, back, st.s);
-    if constexpr (kW) st.w = fmaf(fmaf(-k.shift, s, w), back, st.w);
-    return mx;
+    const float te = exponent(edge, st.m, c2), e = ex2(te);
+    st.s = fmaf(s, back, e);
+    if constexpr (kW) st.w = fmaf(fmaf(-k.shift, s, w), back, e * te);
+    return st;
 }
 
 // The triples of up to 32 lanes as one (the same in every lane).
@@ -530,18 +427,18 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// Where a group's warps, and a cluster's CTAs, leave their triples. The CTAs' slots alternate
-// between rows: a CTA may push its next row's triple while another still reads this row's.
+// Where a group's warps, and a cluster's CTAs, leave their triples. The places alternate between
+// rows: a warp or CTA may leave its next row's triple while another still reads this row's.
 template <int TH>
 struct Joint {
-    float warp[3][TH / 32];
+    float warp[2][3][TH / 32];
     float cta[2][3][kMaxCluster];
 };
 
 // The group's statistics in every thread of it. Contains the group's barrier (before it, threads
 // may leave what the others need after it in shared memory).
 template <int TH, bool kW>
-__device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, float c2) {
+__device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, int parity, float c2) {
     st.s = warp_sum(st.s);
     if constexpr (kW) st.w = warp_sum(st.w);
     if constexpr (TH == 32) {
@@ -549,16 +446,16 @@ __device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, flo
         return st;
     } else {
         const int lane = tid & 31;
-        constexpr int NW = TH / 32;
+        float(&at)[3][TH / 32] = j.warp[parity];
         if (lane == 0) {
-            j.warp[0][tid / 32] = st.m;
-            j.warp[1][tid / 32] = st.s;
-            if constexpr (kW) j.warp[2][tid / 32] = st.w;
+            at[0][tid / 32] = st.m;
+            at[1][tid / 32] = st.s;
+            if constexpr (kW) at[2][tid / 32] = st.w;
         }
         group_sync<TH>();
-        const bool in = lane < NW;
-        return join_lanes<kW>(in ? j.warp[0][lane] : -kInf, in ? j.warp[1][lane] : 0.f,
-                              kW && in ? j.warp[2][lane] : 0.f, c2);
+        const bool in = lane < TH / 32;
+        return join_lanes<kW>(in ? at[0][lane] : -kInf, in ? at[1][lane] : 0.f,
+                              kW && in ? at[2][lane] : 0.f, c2);
     }
 }
 
@@ -585,7 +482,7 @@ __device__ __forceinline__ Stats join_cluster(const Joint<TH>& j, int tid, int c
 template <int TH, bool kW>
 __device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int cluster, int rank,
                                           int parity, float c2) {
-    st = join_group<TH, kW>(j, st, tid, c2);
+    st = join_group<TH, kW>(j, st, tid, parity, c2);
     if (cluster > 1) {
         if (tid < cluster) push_stats<TH, kW>(j, st, rank, tid, parity);
         cluster_sync();
@@ -594,41 +491,32 @@ __device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int c
     return st;
 }
 
-// Registers for a row's vectors: 16 a thread where a warp has a float32 row, so that it holds
-// the audio streams' 2048 logits like a bf16 row's; 8 otherwise.
-template <typename T, int TH>
-__host__ __device__ constexpr int vectors_of() { return TH == 32 && sizeof(T) == 4 ? 16 : 8; }
-
-// CTAs per SM a kernel is compiled for: 64 registers a thread (128 where 64 hold the row).
-template <typename T, int TH>
-__host__ __device__ constexpr int blocks_of() {
-    return TH == 32 ? (sizeof(T) == 4 ? 2 : 3) : 1024 / TH;
-}
-
 template <int TH>
 __host__ __device__ constexpr int block_of() { return TH == 32 ? 256 : TH; }  // warps of short rows share a CTA
+// CTAs per SM a kernel is compiled for: 64 registers a thread
+template <int TH>
+__host__ __device__ constexpr int blocks_of() { return 1024 / block_of<TH>(); }
 
 // ------------------------------------------------------------------ host side
 
+constexpr int kWarpBytes = 8192;            // longest row of a warp
+constexpr int kPartBytes = 72 * 1024;       // a CTA's share that leaves room for three on a SM
+constexpr int kSmemBytes = 227 * 1024;
+
 struct Shape {
-    int threads, cluster;
+    int threads, log_cluster;
 };
 
-// Threads and CTAs for a row of V elements. hold: the row stays in registers between two passes,
-// so it takes as many threads as that needs, then clusters of 512-thread CTAs; a row that is
-// read once is walked in chunks by 256 threads, four CTAs a SM, so that some load while others
-// join their sums. Rows of a small batch are spread over more CTAs.
-inline Shape shape_of(int64_t rows, int V, int size, bool warp_ok, bool hold) {
-    const int per = 16 / size;
-    const int vecs = (V + per - 1) / per + 1;  // rows off a 16-byte boundary have one more
-    if (warp_ok && (V + per - 1) / per <= 32 * (size == 4 ? 16 : 8)) return {32, 1};
-    int cluster = 1;
-    while (hold && cluster < kMaxCluster && vecs > cluster * 512 * 8) cluster *= 2;
-    while (cluster < kMaxCluster && rows * cluster * 2 <= 148 && vecs >= cluster * 2 * 256)
-        cluster *= 2;
-    const int each = (vecs + cluster - 1) / cluster;
-    if (each <= 128 * 8) return {128, cluster};
-    return {each <= 256 * 8 || !hold ? 256 : 512, cluster};
+// Threads and CTAs for a row of V elements: a warp up to 8 KB; else a CTA whose threads have at
+// most about 64 KB / 256 = 256 bytes each; rows over 72 KB, and rows of a batch that would leave
+// SMs idle, are split over a cluster of up to 8 CTAs.
+inline Shape shape_of(int64_t rows, int V, int size, bool warp_ok) {
+    const int64_t bytes = (int64_t)V * size;
+    if (warp_ok && bytes <= kWarpBytes) return {32, 0};
+    int lc = 0;
+    while (lc < 3 && (bytes >> lc) > kPartBytes) ++lc;
+    while (lc < 3 && (rows << (lc + 1)) <= 148 && (bytes >> (lc + 1)) >= 4096) ++lc;
+    return {(bytes >> lc) <= 16384 ? 128 : 256, lc};
 }
 
 inline bool on_device(const void* p, size_t align, int dev) {
@@ -679,34 +567,47 @@ inline bool apart_or_same(const void* x, int64_t ss, int64_t sn, const void* d, 
     return a1 <= b || b1 <= a;
 }
 
-// One launch over all rows: a CTA takes 256 / 32 rows of a warp each, one row, or a
-// cluster's share of one.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_rows(void (*kernel)(KArgs...), int threads, const RowsIn& in, int smem,
-                        cudaStream_t stream, Args... args) {
-    const int block = threads == 32 ? 256 : threads;
-    const int64_t groups = threads == 32 ? (in.rows + 7) / 8 : in.rows;
-    int64_t most = int64_t(1) << 27;  // the kernels loop over the rest
-    if (threads == 32) {              // as many CTAs as are resident: each sets up once
-        int dev = 0, sms = 148, per_sm = 4;
-        if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (groups > (int64_t)sms * 2)
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block, smem);
-        most = (int64_t)sms * (per_sm > 0 ? per_sm : 1);
+// One launch over all rows: as many groups as are resident, each with `slots` places of 16 bytes
+// in dynamic shared memory, or one for each row if they are fewer.
+template <auto kernel, int TH, typename... Args>
+cudaError_t launch_rows(const RowsIn& in, int static_smem, cudaStream_t stream, Args... args) {
+    constexpr int block = block_of<TH>(), rows_per = block / TH;
+    const int smem = rows_per * in.slots * 16;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // raise the kernel's shared-memory limit once per device
+    static unsigned long long configured = 0;  // bit per device
+    if (smem > 48 * 1024 - static_smem && (dev >= 64 || !(configured & (1ull << dev)))) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes - static_smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELAXED);
     }
+    int per_sm = (kSmemBytes + 1024) / (smem + static_smem + 1024);
+    if (per_sm > blocks_of<TH>()) per_sm = blocks_of<TH>();
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    const int64_t groups = (in.rows + rows_per - 1) / rows_per;
+    int64_t most = ((int64_t)sms * per_sm) >> in.log_cluster;
+    if (most < 1) most = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((groups < most ? groups : most) * in.cluster));
+    cfg.gridDim = dim3((unsigned)((groups < most ? groups : most) << in.log_cluster));
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = in.cluster;
+    attr.val.clusterDim.x = 1u << in.log_cluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = in.cluster > 1 ? 1 : 0;
+    cfg.numAttrs = in.log_cluster ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// 16-byte places a group needs for rows of V elements.
+inline int slots_of(int V, int size, int log_cluster) {
+    const int whole = V / (16 / size);
+    return (whole + (1 << log_cluster) - 1) >> log_cluster;
 }
 
 }  // namespace logits

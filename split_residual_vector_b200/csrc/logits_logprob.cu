@@ -9,14 +9,16 @@
 // at least k logits reach costs almost nothing on top of the pass: every
 // thread has its share's maximum anyway, and the k-th largest of those maxima
 // is such a bound (k threads hold a logit that reaches it). One warp finds it by
-// bisecting the values' top 16 bits; only threads whose maximum reaches it look
-// at their logits again and append those that do to a short list, which is
+// bisecting the values' top 16 bits; only warps with a maximum that reaches it
+// look at their logits again and append those that do to a short list, which is
 // ordered by counting. The order of appending has no influence. A list that
 // overflows (rows of few distinct values) is replaced by k rounds that each
 // take the largest key below the last.
 //
 // Gradient: d x_i = c p_i [(z - a) - b (ln p_i + H)] + c a [i = token] from the
-// vectors in registers, so that the row is read once and written once.
+// row in shared memory, so that it is read once from global memory and written
+// once. What decides whether a row is needed at all (its token and upstream
+// gradients) is loaded a row ahead of its logits.
 #include "logits.cuh"
 
 namespace mimi {
@@ -66,10 +68,11 @@ __device__ __forceinline__ float order_value(uint32_t o) {
 __device__ __forceinline__ float key_value(Key key) { return order_value((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int key_id(Key key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
-// The row's target, -1 if it has none; count: add a token past V to n_bad.
-__device__ __forceinline__ int target_of(const TokensIn& tk, int64_t s, int j, int V, bool count) {
-    if (tk.tok == nullptr) return -1;
-    const int32_t t = __ldg(tk.tok + s * tk.ss + j * tk.sn);
+__device__ __forceinline__ int32_t token_at(const TokensIn& tk, const RowWalk& row, int64_t rows) {
+    return tk.tok == nullptr || row.r >= rows ? -1 : __ldg(tk.tok + row.s * tk.ss + row.j * tk.sn);
+}
+// A row's target by its token, -1 if it has none; count: add a token past V to n_bad.
+__device__ __forceinline__ int target_of(const TokensIn& tk, int32_t t, int V, bool count) {
     if (t < 0 || t == tk.pad) return -1;
     if (t >= V) {
         if (count && tk.n_bad != nullptr) atomicAdd(tk.n_bad, 1ull);
@@ -103,8 +106,6 @@ struct TopShared {
     int count;
     alignas(16) Key list[kCap + 8];
     Key last[TH / 32];
-    // the threads' maxima of chunk c (and c + 8, ...), for parts of several chunks
-    float of_chunk[TH == 32 ? 1 : 8][TH == 32 ? 1 : TH];
 };
 template <int TH>
 struct TopLists {  // the keys that a cluster's CTAs give its first one
@@ -124,12 +125,26 @@ __device__ __forceinline__ void leave_maxima(TopShared<TH>& sh, float top, int t
     }
 }
 
-// The part's logits that reach the bound, as unordered keys in sh.list: returns their number,
-// at least min(k, the logits above -inf); past kCap the list is not complete. `v` holds the part
-// where it is one chunk.
-template <int TH, int NV, typename T>
-__device__ __forceinline__ int collect(TopShared<TH>& sh, const Part<T>& p, uint32_t (&v)[NV][4],
-                                       float top, int tid, int k) {
+// f(value, id) for this thread's logits of the share.
+template <int TH, typename T, typename F>
+__device__ __forceinline__ void each_logit(const uint4* buf, const Part<T>& p, int tid, float edge,
+                                           F&& f) {
+#pragma unroll 1
+    for (int i = tid; i < p.nv; i += TH) {
+        const uint4 q = buf[i];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < Part<T>::kPer; ++j)
+            f(element<T>(w, j), p.first + i * Part<T>::kPer + j);
+    }
+    if (edge > -kInf) f(edge, p.edge(tid));
+}
+
+// The share's logits that reach the bound, as unordered keys in sh.list: returns their number,
+// at least min(k, the logits above -inf); past kCap the list is not complete.
+template <int TH, typename T>
+__device__ __forceinline__ int collect(TopShared<TH>& sh, const Part<T>& p, const uint4* buf,
+                                       float edge, float top, int tid, int k) {
     constexpr int kN = TopShared<TH>::kGroups / 32, kCap = TopShared<TH>::kCap;
     if (tid < 32) {
         uint32_t q[kN];
@@ -165,15 +180,9 @@ __device__ __forceinline__ int collect(TopShared<TH>& sh, const Part<T>& p, uint
     group_sync<TH>();
     const float bound = sh.bound;
     const int lane = tid & 31;
-    // a chunk's logits (each lane's own) that reach the bound: counted, then given places
-    auto append = [&](int base) {
+    if (__any_sync(kFull, top >= bound)) {  // count each lane's, then give them places
         int mine = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!__any_sync(kFull, vector_max<T>(v[i]) >= bound)) continue;
-#pragma unroll
-            for (int j = 0; j < Part<T>::kPer; ++j) mine += element<T>(v[i], j) >= bound;
-        }
+        if (top >= bound) each_logit<TH>(buf, p, tid, edge, [&](float x, int) { mine += x >= bound; });
         int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -183,34 +192,13 @@ __device__ __forceinline__ int collect(TopShared<TH>& sh, const Part<T>& p, uint
         int at = 0;
         if (lane == 31) at = atomicAdd(&sh.count, upto);
         at = __shfl_sync(kFull, at, 31) + upto - mine;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!__any_sync(kFull, vector_max<T>(v[i]) >= bound)) continue;
-#pragma unroll
-            for (int j = 0; j < Part<T>::kPer; ++j) {
-                const float x = element<T>(v[i], j);
+        if (mine)
+            each_logit<TH>(buf, p, tid, edge, [&](float x, int id) {
                 if (x >= bound) {
-                    if (at < kCap) sh.list[at] = key_of(x, p.first(base + i * TH + tid) + j);
+                    if (at < kCap) sh.list[at] = key_of(x, id);
                     ++at;
                 }
-            }
-        }
-    };
-    if (__any_sync(kFull, top >= bound)) {
-        if (TH == 32 ? p.size() <= 32 * NV : p.size() <= TH * NV) {
-            append(p.v0);
-        } else {  // every lane goes through its own chunks
-            const int chunks = (p.size() + TH * NV - 1) / (TH * NV);
-            int c = -1;
-            while (true) {
-                do ++c;
-                while (TH > 32 && c < chunks && sh.of_chunk[c % 8][tid] < bound);
-                if (!__any_sync(kFull, c < chunks)) break;
-                const int base = c < chunks ? p.v0 + c * TH * NV : p.v1;  // v1: nothing
-                load_chunk<TH, NV>(p, base, tid, v);
-                append(base);
-            }
-        }
+            });
     }
     group_sync<TH>();
     return sh.count;
@@ -231,26 +219,18 @@ __device__ __forceinline__ void order_list(TopShared<TH>& sh, int n, int tid, in
     }
 }
 
-// The k largest of the part without a list: k rounds that each find the largest key below the
+// The k largest of the share without a list: k rounds that each find the largest key below the
 // last one; returns how many there are (one thread puts them).
-template <int TH, int NV, typename T, typename Put>
-__device__ __noinline__ int take_rounds(TopShared<TH>& sh, const Part<T> p, int tid, int k,
-                                        Put put) {
+template <int TH, typename T, typename Put>
+__device__ __noinline__ int take_rounds(TopShared<TH>& sh, const Part<T> p, const uint4* buf,
+                                        float edge, int tid, int k, Put put) {
     Key last = ~Key(0);
     for (int q = 0; q < k; ++q) {
         Key best = 0;
-        for (int base = p.v0; base < p.v1; base += TH * NV) {
-            uint32_t v[NV][4];
-            load_chunk<TH, NV>(p, base, tid, v);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < Part<T>::kPer; ++j) {
-                    const float x = element<T>(v[i], j);
-                    const Key key = key_of(x, p.first(base + i * TH + tid) + j);
-                    if (x > -kInf && key < last && key > best) best = key;
-                }
-        }
+        each_logit<TH>(buf, p, tid, edge, [&](float x, int id) {
+            const Key key = key_of(x, id);
+            if (x > -kInf && key < last && key > best) best = key;
+        });
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             const Key other = __shfl_xor_sync(kFull, best, o);
@@ -272,51 +252,66 @@ __device__ __noinline__ int take_rounds(TopShared<TH>& sh, const Part<T> p, int 
 // ------------------------------------------------------------------ forward
 
 template <typename T, int TH, bool kTop>
-__global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
+__global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
     k_logprob(RowsIn in, TokensIn tk, ValuesOut o) {
-    constexpr int NV = vectors_of<T, TH>(), kRows = block_of<TH>() / TH;
+    constexpr int kRows = block_of<TH>() / TH;
+    extern __shared__ uint4 buffers[];  // [groups][slots]
     __shared__ Joint<TH> joint[kRows];
     __shared__ TopShared<kTop ? TH : 32> tops[kTop ? kRows : 1];
     __shared__ TopLists<kTop ? TH : 32> lists;
     const int tid = TH == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int group = TH == 32 ? threadIdx.x / 32 : 0;
-    const int rank = in.cluster > 1 ? (int)cluster_ctarank() : 0;
+    const int lc = TH == 32 ? 0 : in.log_cluster, cluster = 1 << lc;
+    const int rank = lc ? (int)cluster_ctarank() : 0;
+    const bool first_warp = rank == 0 && tid < 32;  // has the row's edges
+    uint4* buf = buffers + (size_t)group * in.slots;
     const float c2 = in.c * kLog2e;
-    const int64_t step = (int64_t)(gridDim.x / in.cluster) * kRows;
-    if (in.cluster > 1) cluster_arrive();  // every CTA runs before one writes to another
-    bool started = in.cluster == 1;
-    RowWalk at_row((int64_t)(blockIdx.x / in.cluster) * kRows + group, step, in.n);
-    for (; at_row.r < in.rows; at_row.next(in.n)) {
-        const int64_t r = at_row.r, s = at_row.s;
-        const int j = at_row.j;
-        const Part<T> p(static_cast<const T*>(in.x) + s * in.ss + j * in.sn, in.V, rank, in.cluster);
-        uint32_t v[NV][4];
-        load_chunk<TH, NV>(p, p.v0, tid, v);
+    if (lc) cluster_arrive();  // every CTA runs before one writes to another
+    bool started = lc == 0;
+    RowWalk row((int64_t)(blockIdx.x >> lc) * kRows + group,
+                (int64_t)(gridDim.x >> lc) * kRows, in.n);
+    auto part_at = [&]() {
+        return Part<T>(static_cast<const T*>(in.x) + row.s * in.ss + row.j * in.sn, in.V, rank, lc);
+    };
+    auto edge_of = [&](const Part<T>& p) {
+        const int i = first_warp ? p.edge(tid) : -1;
+        return i < 0 ? -kInf : widen(p.x[i]);
+    };
+    if (row.r >= in.rows) {
+        if (!started) cluster_wait();
+        return;
+    }
+    Part<T> p = part_at();
+    fetch<TH>(buf, p, tid);
+    float edge = edge_of(p);
+    const bool teller = first_warp && tid == 0;
+    int32_t token = teller ? token_at(tk, row, in.rows) : -1;
+    for (int parity = 0;; parity ^= 1) {
+        const int64_t r = row.r;
         int t = -1;
         float xt = 0.f;
-        if (tid == 0 && rank == 0) {
-            t = target_of(tk, s, j, in.V, true);
+        if (teller) {
+            t = target_of(tk, token, in.V, true);
             if (t >= 0) xt = widen(p.x[t]);
         }
-        Stats st{-kInf, 0.f, 0.f};
-        float top = -kInf;
-        for (int base = p.v0; base < p.v1; base += TH * NV) {
-            if (base != p.v0) load_chunk<TH, NV>(p, base, tid, v);
-            const float mx = add_chunk<TH, NV, true, T>(p, base, tid, v, c2, st);
-            if constexpr (kTop) {
-                top = fmaxf(top, mx);
-                if (TH > 32 && p.size() > TH * NV) {
-                    const int q = (base - p.v0) / (TH * NV);
-                    float& of = tops[group].of_chunk[q % 8][tid];
-                    of = q < 8 ? mx : fmaxf(of, mx);
-                }
-            }
-        }
+        arrived();
+        float top;
+        Stats st = pass<TH, true, T>(buf, p.nv, tid, edge, c2, top);
+        row.next(in.n);
+        const bool more = row.r < in.rows;
+        auto send_next = [&]() {
+            if (!more) return;
+            p = part_at();
+            fetch<TH>(buf, p, tid);
+            edge = edge_of(p);
+            if (teller) token = token_at(tk, row, in.rows);
+        };
         if constexpr (kTop) leave_maxima<TH>(tops[group], top, tid);
-        st = join_group<TH, true>(joint[group], st, tid, c2);
+        else send_next();
+        st = join_group<TH, true>(joint[group], st, tid, parity, c2);
         int n = 0;
-        if constexpr (kTop) n = collect<TH, NV>(tops[group], p, v, top, tid, o.k);
-        if (TH > 32 && in.cluster > 1) {  // the first CTA gets the others' triples and keys
+        if constexpr (kTop) n = collect<TH>(tops[group], p, buf, edge, top, tid, o.k);
+        if (TH > 32 && lc) {  // the first CTA gets the others' triples and keys
             if (!started) cluster_wait();
             started = true;
             if (tid == 0) push_stats<TH, true>(joint[0], st, rank, 0, 0);
@@ -324,7 +319,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
                 const uint32_t to = cluster_map(smem_u32(&lists.of[rank][0]), 0);
                 auto give = [to](int place, Key key) { st_cluster_u64(to + 8 * place, key); };
                 if (n > TopShared<TH>::kCap) {
-                    n = take_rounds<TH, NV>(tops[0], p, tid, o.k, give);
+                    n = take_rounds<TH>(tops[0], p, buf, edge, tid, o.k, give);
                 } else if (n > kMaxTop) {
                     order_list(tops[0], n, tid, o.k, give);
                     n = o.k;
@@ -332,9 +327,10 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
                     for (int i = tid; i < n; i += TH) give(i, tops[0].list[i]);
                 }
                 if (tid == 0) st_cluster_u32(cluster_map(smem_u32(&lists.count[rank]), 0), n);
+                send_next();
             }
             cluster_sync();
-            if (rank == 0) st = join_cluster<TH, true>(joint[0], tid, in.cluster, 0, c2);
+            if (rank == 0) st = join_cluster<TH, true>(joint[0], tid, cluster, 0, c2);
         }
         if (rank == 0) {
             if (tid == 0) put_values(o, r, t, xt, in.c, st);
@@ -348,28 +344,25 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
                         o.top_logprob[at + place] =
                             broken ? NAN : key ? log_prob(key_value(key), in.c, st.m, ln_s) : -kInf;
                 };
-                if (broken) {
+                const bool over = n > TopShared<TH>::kCap;
+                if (lc) {
                     n = 0;
-                } else if (in.cluster == 1) {
-                    if (n > TopShared<TH>::kCap) n = take_rounds<TH, NV>(tops[group], p, tid, o.k, out);
-                    else order_list(tops[group], n, tid, o.k, out);
-                } else {
-                    n = 0;
-                    for (int l = 0; l < in.cluster; ++l) {
+                    for (int l = 0; l < cluster; ++l) {
                         for (int e = tid; e < lists.count[l]; e += TH)
                             tops[0].list[n + e] = lists.of[l][e];
                         n += lists.count[l];
                     }
-                    order_list(tops[0], n, tid, o.k, out);
+                } else if (over && !broken) {
+                    n = take_rounds<TH>(tops[group], p, buf, edge, tid, o.k, out);
                 }
+                if (!lc) send_next();
+                if (broken) n = 0;
+                else if (lc || !over) order_list(tops[group], n, tid, o.k, out);
                 for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
             }
         }
-        if (TH > 32 && in.cluster > 1) {
-            if (r + step < in.rows) cluster_sync();  // the lists are free again
-        } else {
-            group_sync<TH>();
-        }
+        if (!more) break;
+        if (lc) cluster_sync();  // the first CTA has read what the others gave it
     }
     if (!started) cluster_wait();
 }
@@ -377,96 +370,121 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>())
 // ------------------------------------------------------------------ gradient
 
 template <typename T, int TH>
-__global__ void __launch_bounds__(block_of<TH>(), blocks_of<T, TH>()) k_logprob_grad(RowsIn in, TokensIn tk, GradIn g,
-                                                               ValuesOut o) {
-    constexpr int NV = vectors_of<T, TH>(), kRows = block_of<TH>() / TH, kPer = Part<T>::kPer;
+__global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
+    k_logprob_grad(RowsIn in, TokensIn tk, GradIn g, ValuesOut o) {
+    constexpr int kRows = block_of<TH>() / TH, kPer = Part<T>::kPer;
+    extern __shared__ uint4 buffers[];  // [groups][slots]
     __shared__ Joint<TH> joint[kRows];
     const int tid = TH == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int group = TH == 32 ? threadIdx.x / 32 : 0;
-    const int rank = in.cluster > 1 ? (int)cluster_ctarank() : 0;
+    const int lc = TH == 32 ? 0 : in.log_cluster, cluster = 1 << lc;
+    const int rank = lc ? (int)cluster_ctarank() : 0;
+    const bool first_warp = rank == 0 && tid < 32;
+    uint4* buf = buffers + (size_t)group * in.slots;
     const float c2 = in.c * kLog2e;
     const bool values = o.logprob != nullptr || o.entropy != nullptr || o.lse != nullptr;
-    int parity = 0;
-    if (in.cluster > 1) cluster_sync();
-    RowWalk at_row((int64_t)(blockIdx.x / in.cluster) * kRows + group,
-                   (int64_t)(gridDim.x / in.cluster) * kRows, in.n);
-    for (; at_row.r < in.rows; at_row.next(in.n)) {
-        const int64_t r = at_row.r, s = at_row.s;
-        const int j = at_row.j;
-        const Part<T> p(static_cast<const T*>(in.x) + s * in.ss + j * in.sn, in.V, rank, in.cluster);
-        // the gradient's row has its own alignment
-        T* d = static_cast<T*>(g.d) + s * g.ss + j * g.sn;
-        const bool wide = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(p.x)) & 15u) == 0;
-        const int t = target_of(tk, s, j, in.V, tid == 0 && rank == 0);
-        const float a = (t < 0 || g.g_logprob == nullptr) ? 0.f : __ldg(g.g_logprob + r);
-        const float b = g.g_entropy == nullptr ? 0.f : __ldg(g.g_entropy + r);
-        const float z = g.g_lse == nullptr ? 0.f : __ldg(g.g_lse + r);
-        const bool zero = a == 0.f && b == 0.f && z == 0.f;
-        uint32_t v[NV][4];
-        Stats st{-kInf, 0.f, 0.f};
-        const bool owner = t >= 0 && p.holds(p.vector_of(t)) && (p.vector_of(t) - p.v0) % TH == tid;
-        float xt = 0.f;
-        if (!zero || values) {
-            load_chunk<TH, NV>(p, p.v0, tid, v);
-            if (t >= 0 && (owner || (tid == 0 && rank == 0))) xt = widen(p.x[t]);
-            for (int base = p.v0; base < p.v1; base += TH * NV) {
-                if (base != p.v0) load_chunk<TH, NV>(p, base, tid, v);
-                add_chunk<TH, NV, true, T>(p, base, tid, v, c2, st);
-            }
-            st = join_row<TH, true>(joint[group], st, tid, in.cluster, rank, parity, c2);
-            parity ^= 1;
-            if (tid == 0 && rank == 0) put_values(o, r, t, xt, in.c, st);
+    if (lc) cluster_sync();  // every CTA runs before one writes to another
+    RowWalk row((int64_t)(blockIdx.x >> lc) * kRows + group,
+                (int64_t)(gridDim.x >> lc) * kRows, in.n);
+    // what the row's gradient comes from: loaded a row ahead
+    struct Up {
+        int32_t token;
+        float a, b, z;
+    };
+    auto up_at = [&]() {
+        Up u{token_at(tk, row, in.rows), 0.f, 0.f, 0.f};
+        if (row.r < in.rows) {
+            if (g.g_logprob != nullptr) u.a = __ldg(g.g_logprob + row.r);
+            if (g.g_entropy != nullptr) u.b = __ldg(g.g_entropy + row.r);
+            if (g.g_lse != nullptr) u.z = __ldg(g.g_lse + row.r);
         }
-        const bool none = zero || st.s == 0.f;
-        const float inv = none ? 0.f : reciprocal(st.s), ln_s = none ? 0.f : ln(st.s);
-        const float h = ln_s - kLn2 * (st.w * inv);
+        return u;
+    };
+    auto part_at = [&]() {
+        return Part<T>(static_cast<const T*>(in.x) + row.s * in.ss + row.j * in.sn, in.V, rank, lc);
+    };
+    Up up = up_at();
+    for (int parity = 0; row.r < in.rows;) {
+        const int64_t r = row.r;
+        const Part<T> p = part_at();
+        // the gradient's row has its own alignment
+        T* d = static_cast<T*>(g.d) + row.s * g.ss + row.j * g.sn;
+        const bool wide = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(p.x)) & 15u) == 0;
+        const int t = target_of(tk, up.token, in.V, first_warp && tid == 0);
+        const float a = t < 0 ? 0.f : up.a, b = up.b, z = up.z;
+        const bool zero = a == 0.f && b == 0.f && z == 0.f;
+        row.next(in.n);
+        const int ie = first_warp ? p.edge(tid) : -1;
+        float edge = -kInf, xt = 0.f;
+        if (!zero || values) {
+            fetch<TH>(buf, p, tid);
+            if (ie >= 0) edge = widen(p.x[ie]);
+            if (t >= 0) xt = widen(p.x[t]);
+        }
+        up = up_at();
+        Stats st{-kInf, 0.f, 0.f};
+        if (!zero || values) {
+            arrived();
+            float top;
+            st = pass<TH, true, T>(buf, p.nv, tid, edge, c2, top);
+            st = join_row<TH, true>(joint[group], st, tid, cluster, rank, parity, c2);
+            parity ^= 1;
+            if (first_warp && tid == 0) put_values(o, r, t, xt, in.c, st);
+        }
+        T* out = d + p.first;
+        if (zero || st.s == 0.f) {
+            for (int i = tid; i < p.nv; i += TH) {
+                const float y[kPer] = {};
+                store_vector<T>(out + (size_t)i * kPer, wide, y);
+            }
+            if (ie >= 0) narrow(0.f, d + ie);
+            continue;
+        }
+        const float inv = reciprocal(st.s), ln_s = ln(st.s), h = ln_s - kLn2 * (st.w * inv);
         // c p_i [(z - a) - b (ln p_i + H)] = 2^t (c0 + c1 t), t = log2(e) c (x - m)
         const float c0 = in.c * inv * ((z - a) - b * (h - ln_s)), c1 = -in.c * inv * b * kLn2;
         const Scale k(c2, st.m);
         const float back = ex2(-k.shift);  // the same for t that are off by the shift
         const float k0 = back * fmaf(-k.shift, c1, c0), k1 = back * c1;
-        for (int base = p.v0; base < p.v1; base += TH * NV) {
-            if (!none && p.size() > TH * NV) load_chunk<TH, NV>(p, base, tid, v);
-            store_chunk<TH, NV>(p, base, tid, d, wide, v, [&](const uint32_t (&w)[4], float (&y)[kPer]) {
-                if (none) {
+        each_vector<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
+            Pair q[kPer / 2];
+            float y[kPer];
+            exponents<T, true>(w, k, q);
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) y[e] = 0.f;
-                } else {
-                    Pair q[kPer / 2];
-                    exponents<T, true>(w, k, q);
-#pragma unroll
-                    for (int e = 0; e < kPer / 2; ++e)
-                        halves(mul2(ex2_pair(q[e]), fma2(pair_of(k1, k1), q[e], pair_of(k0, k0))),
-                               y[2 * e], y[2 * e + 1]);
-                }
-            });
-        }
-        if (owner && !none) {
-            const float e = exponent(xt, st.m, c2);
-            narrow(fmaf(ex2(e), fmaf(c1, e, c0), in.c * a), d + t);
-        }
-        group_sync<TH>();
+            for (int e = 0; e < kPer / 2; ++e)
+                halves(mul2(ex2_pair(q[e]), fma2(pair_of(k1, k1), q[e], pair_of(k0, k0))),
+                       y[2 * e], y[2 * e + 1]);
+            store_vector<T>(out + (size_t)i * kPer, wide, y);
+        });
+        auto one = [&](float x) {
+            const float e = exponent(x, st.m, c2);
+            return ex2(e) * fmaf(c1, e, c0);
+        };
+        if (ie >= 0) narrow(one(edge) + (ie == t ? in.c * a : 0.f), d + ie);
+        // the target's own term, by the thread that stored its vector
+        const int at = t >= 0 ? p.place(t) : -1;
+        if (at >= 0 && at / kPer % TH == tid) narrow(one(xt) + in.c * a, d + t);
     }
 }
 
 template <typename T, bool kTop>
-cudaError_t forward_of(const Shape& sh, const RowsIn& in, const TokensIn& tk, const ValuesOut& o,
+cudaError_t forward_of(int threads, const RowsIn& in, const TokensIn& tk, const ValuesOut& o,
                        cudaStream_t s) {
-    switch (sh.threads) {
-        case 32: return launch_rows(k_logprob<T, 32, kTop>, 32, in, 0, s, in, tk, o);
-        case 128: return launch_rows(k_logprob<T, 128, kTop>, 128, in, 0, s, in, tk, o);
-        default: return launch_rows(k_logprob<T, 256, kTop>, 256, in, 0, s, in, tk, o);
+    constexpr int kLists = kTop ? 18 * 1024 : 1024;  // static shared memory, rounded up
+    switch (threads) {
+        case 32: return launch_rows<&k_logprob<T, 32, kTop>, 32>(in, kTop ? 10 * 1024 : 512, s, in, tk, o);
+        case 128: return launch_rows<&k_logprob<T, 128, kTop>, 128>(in, kLists, s, in, tk, o);
+        default: return launch_rows<&k_logprob<T, 256, kTop>, 256>(in, kLists, s, in, tk, o);
     }
 }
 
 template <typename T>
-cudaError_t gradient_of(const Shape& sh, const RowsIn& in, const TokensIn& tk, const GradIn& g,
+cudaError_t gradient_of(int threads, const RowsIn& in, const TokensIn& tk, const GradIn& g,
                         const ValuesOut& o, cudaStream_t s) {
-    switch (sh.threads) {
-        case 32: return launch_rows(k_logprob_grad<T, 32>, 32, in, 0, s, in, tk, g, o);
-        case 128: return launch_rows(k_logprob_grad<T, 128>, 128, in, 0, s, in, tk, g, o);
-        case 256: return launch_rows(k_logprob_grad<T, 256>, 256, in, 0, s, in, tk, g, o);
-        default: return launch_rows(k_logprob_grad<T, 512>, 512, in, 0, s, in, tk, g, o);
+    switch (threads) {
+        case 32: return launch_rows<&k_logprob_grad<T, 32>, 32>(in, 4096, s, in, tk, g, o);
+        case 128: return launch_rows<&k_logprob_grad<T, 128>, 128>(in, 1024, s, in, tk, g, o);
+        default: return launch_rows<&k_logprob_grad<T, 256>, 256>(in, 1024, s, in, tk, g, o);
     }
 }
 
@@ -494,16 +512,17 @@ extern "C" int mimi_rvq_token_logprob(const void* logits, int dtype, int64_t S, 
     if (top_k > 0 && (!maybe_on_device(top_ids, 4, dev) || !maybe_on_device(top_logprob, 4, dev)))
         return MIMI_RVQ_EINVAL;
     const int k = top_ids != nullptr || top_logprob != nullptr ? top_k : 0;
-    const Shape sh = shape_of(S * n, V, size, k <= kWarpTop, false);
-    const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.cluster};
+    const Shape sh = shape_of(S * n, V, size, k <= kWarpTop);
+    const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
+                    slots_of(V, size, sh.log_cluster)};
     const TokensIn tk{tokens, tok_stride_s, tok_stride_n, pad,
                       reinterpret_cast<unsigned long long*>(n_bad)};
     const ValuesOut o{logprob, entropy, lse, top_ids, top_logprob, k};
     if (dtype == MIMI_RVQ_BF16)
-        return status_of(k ? forward_of<__nv_bfloat16, true>(sh, in, tk, o, stream)
-                           : forward_of<__nv_bfloat16, false>(sh, in, tk, o, stream));
-    return status_of(k ? forward_of<float, true>(sh, in, tk, o, stream)
-                       : forward_of<float, false>(sh, in, tk, o, stream));
+        return status_of(k ? forward_of<__nv_bfloat16, true>(sh.threads, in, tk, o, stream)
+                           : forward_of<__nv_bfloat16, false>(sh.threads, in, tk, o, stream));
+    return status_of(k ? forward_of<float, true>(sh.threads, in, tk, o, stream)
+                       : forward_of<float, false>(sh.threads, in, tk, o, stream));
 }
 
 extern "C" int mimi_rvq_token_logprob_grad(
@@ -529,12 +548,13 @@ extern "C" int mimi_rvq_token_logprob_grad(
         !maybe_on_device(logprob, 4, dev) || !maybe_on_device(entropy, 4, dev) ||
         !maybe_on_device(lse, 4, dev) || !maybe_on_device(n_bad, 8, dev))
         return MIMI_RVQ_EINVAL;
-    const Shape sh = shape_of(S * n, V, size, true, true);
-    const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.cluster};
+    const Shape sh = shape_of(S * n, V, size, true);
+    const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
+                    slots_of(V, size, sh.log_cluster)};
     const TokensIn tk{tokens, tok_stride_s, tok_stride_n, pad,
                       reinterpret_cast<unsigned long long*>(n_bad)};
     const GradIn g{g_logprob, g_entropy, g_lse, dlogits, d_stride_s, d_stride_n};
     const ValuesOut o{logprob, entropy, lse, nullptr, nullptr, 0};
-    return status_of(dtype == MIMI_RVQ_BF16 ? gradient_of<__nv_bfloat16>(sh, in, tk, g, o, stream)
-                                            : gradient_of<float>(sh, in, tk, g, o, stream));
+    return status_of(dtype == MIMI_RVQ_BF16 ? gradient_of<__nv_bfloat16>(sh.threads, in, tk, g, o, stream)
+                                            : gradient_of<float>(sh.threads, in, tk, g, o, stream));
 }

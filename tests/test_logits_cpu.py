@@ -23,7 +23,7 @@ def lib():
 
 ROWS = dict(dtype=0, S=0, n=1, V=100, ss=100, sn=0)
 BAD_ROWS = [dict(dtype=2), dict(dtype=-1), dict(S=-1), dict(n=-1), dict(n=65537), dict(V=0),
-            dict(V=-5), dict(V=(1 << 20) + 1), dict(ss=-1), dict(sn=-1), dict(S=1 << 41),
+            dict(V=-5), dict(V=(3 << 17) + 1), dict(ss=-1), dict(sn=-1), dict(S=1 << 41),
             dict(sn=1 << 60)]
 
 
@@ -59,6 +59,7 @@ def test_sizes_are_checked_before_anything_else(lib, call):
     assert call(lib) == OK
     assert call(lib, n=0) == OK
     assert call(lib, V=1, ss=1) == OK
+    assert call(lib, V=3 << 17, ss=3 << 17) == OK
     for over in BAD_ROWS:
         assert call(lib, **over) == EINVAL, over
     for scale in (0.0, -1.0, math.inf, math.nan):

@@ -61,7 +61,7 @@ def check_values(r, x, tokens, pad=-1, c=1.0, k=0):
 SHAPES = [(1, 0, 1), (3, 0, 2), (5, 1, 7), (2, 3, 8), (4, 0, 31), (3, 2, 64), (2, 0, 255),
           (3, 5, 257), (9, 0, 1000), (130, 3, 2047), (37, 8, 2048), (11, 1, 2049), (5, 0, 4097),
           (3, 0, 8192), (1, 0, 10007), (2, 0, 16385), (1, 0, 32000), (300, 0, 32000),
-          (7, 0, 32001), (2, 0, 65537), (1, 0, 131072), (3, 0, 262147), (1, 0, 1 << 20)]
+          (7, 0, 32001), (2, 0, 65537), (1, 0, 131072), (3, 0, 262147), (2, 0, 3 << 17)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
