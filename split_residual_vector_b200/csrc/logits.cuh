@@ -154,7 +154,7 @@ struct Scale {
         far = !(fabsf(ref) < 32768.f && c2 > 1.0e-33f && c2 < 1.0e30f);
         shift = far ? 0.f : fmaf(m, c2, -ref);
         const float f = __fdividef(ref + kLow, c2);
-        floor_bf16x2 = far ? 0xFF80FF80u : pack_bf16x2(f, f);  // far: no floor here
+        floor_bf16x2 = pack_bf16x2(f, f);
     }
 };
 __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
@@ -162,7 +162,7 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-template <typename T, bool kFinite>
+template <typename T, bool kFinite, bool kFar>
 __device__ __forceinline__ void exponents(const uint32_t (&w)[4], const Scale& k,
                                           Pair (&t)[Elem<T>::kPer / 2]) {
     constexpr int kPairs = Elem<T>::kPer / 2;
@@ -171,11 +171,11 @@ __device__ __forceinline__ void exponents(const uint32_t (&w)[4], const Scale& k
         if constexpr (sizeof(T) == 4) {
             t[j] = pair_of(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
         } else {
-            const uint32_t u = kFinite ? max_nan_bf16x2(w[j], k.floor_bf16x2) : w[j];
+            const uint32_t u = kFinite && !kFar ? max_nan_bf16x2(w[j], k.floor_bf16x2) : w[j];
             t[j] = pair_of(bf16_lo_to_f32(u), bf16_hi_to_f32(u));
         }
     }
-    if (!k.far) {
+    if constexpr (!kFar) {
         const Pair c = pair_of(k.c2, k.c2), r = pair_of(-k.ref, -k.ref);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) t[j] = fma2(t[j], c, r);
@@ -184,7 +184,7 @@ __device__ __forceinline__ void exponents(const uint32_t (&w)[4], const Scale& k
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) t[j] = mul2(add2(t[j], m), c);
     }
-    if (kFinite && (sizeof(T) == 4 || k.far))
+    if constexpr (kFinite && (sizeof(T) == 4 || kFar))
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
             float a, b;
@@ -314,7 +314,17 @@ __device__ __forceinline__ void store_vector(T* at, bool wide, const float (&y)[
     }
 }
 
-// f(i, vector i of the share) for this thread's vectors, in groups of four.
+// f(i, vector i of the share) for this thread's vectors, one after another.
+template <int TH, typename F>
+__device__ __forceinline__ void each_in_turn(const uint4* buf, int nv, int tid, F&& f) {
+#pragma unroll 1
+    for (int i = tid; i < nv; i += TH) {
+        const uint4 q = buf[i];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        f(i, w);
+    }
+}
+// the same in groups of four
 template <int TH, typename F>
 __device__ __forceinline__ void each_vector(const uint4* buf, int nv, int tid, F&& f) {
     int i = tid;
@@ -371,16 +381,26 @@ __device__ __forceinline__ Stats pass(const uint4* buf, int nv, int tid, float e
     Stats st{warp_max(top), 0.f, 0.f};
     const Scale k(c2, st.m);
     Pair s2 = 0, w2 = 0;  // (0, 0)
-    each_vector<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
-        Pair t[Elem<T>::kPer / 2];
-        exponents<T, kW>(w, k, t);
+    auto add = [&](const Pair (&t)[Elem<T>::kPer / 2]) {
 #pragma unroll
         for (int j = 0; j < Elem<T>::kPer / 2; ++j) {
             const Pair e = ex2_pair(t[j]);
             s2 = add2(s2, e);
             if constexpr (kW) w2 = fma2(e, t[j], w2);
         }
-    });
+    };
+    if (!k.far)
+        each_vector<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
+            Pair t[Elem<T>::kPer / 2];
+            exponents<T, kW, false>(w, k, t);
+            add(t);
+        });
+    else
+        each_in_turn<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
+            Pair t[Elem<T>::kPer / 2];
+            exponents<T, kW, true>(w, k, t);
+            add(t);
+        });
     float s, s1, w = 0.f, w1 = 0.f;
     halves(s2, s, s1);
     s += s1;

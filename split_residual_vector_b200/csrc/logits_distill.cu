@@ -302,16 +302,27 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
                 // a rest of -inf only has no gradient of its own: 2^t is 0 there
                 const float f0 = gc * (Q * inv * (rest.s == 0.f ? 1.f : ex2((rest.m - all.m) * c2))
                                        - (qr > 0.f ? qr / rest.s : 0.f));
-                const float f = f0 * ex2(-k.shift);
-                each_vector<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
-                    Pair t[kPer / 2];
+                const bool fast = !k.far && wide;
+                const float f = fast ? f0 * ex2(-k.shift) : f0;
+                auto put = [&](int i, const Pair (&t)[kPer / 2], bool whole) {
                     float y[kPer];
-                    exponents<T, false>(w, k, t);
 #pragma unroll
                     for (int e = 0; e < kPer / 2; ++e)
                         halves(mul2(ex2_pair(t[e]), pair_of(f, f)), y[2 * e], y[2 * e + 1]);
-                    store_vector<T>(out + (size_t)i * kPer, wide, y);
-                });
+                    store_vector<T>(out + (size_t)i * kPer, whole, y);
+                };
+                if (fast)
+                    each_vector<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
+                        Pair t[kPer / 2];
+                        exponents<T, false, false>(w, k, t);
+                        put(i, t, true);
+                    });
+                else
+                    each_in_turn<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
+                        Pair t[kPer / 2];
+                        exponents<T, false, true>(w, k, t);
+                        put(i, t, wide);
+                    });
                 if (ie >= 0) narrow(ex2(exponent(edge, rest.m, c2)) * f0, d + ie);
                 group_sync<TH>();  // the listed tokens' places hold the rest's gradient by now
                 if (tid < 32)

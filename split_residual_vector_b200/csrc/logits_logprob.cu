@@ -444,18 +444,29 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
         // c p_i [(z - a) - b (ln p_i + H)] = 2^t (c0 + c1 t), t = log2(e) c (x - m)
         const float c0 = in.c * inv * ((z - a) - b * (h - ln_s)), c1 = -in.c * inv * b * kLn2;
         const Scale k(c2, st.m);
-        const float back = ex2(-k.shift);  // the same for t that are off by the shift
-        const float k0 = back * fmaf(-k.shift, c1, c0), k1 = back * c1;
-        each_vector<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
-            Pair q[kPer / 2];
+        const bool fast = !k.far && wide;
+        const float shift = fast ? k.shift : 0.f, back = ex2(-shift);
+        const float k0 = back * fmaf(-shift, c1, c0), k1 = back * c1;  // for t off by the shift
+        auto put = [&](int i, const Pair (&q)[kPer / 2], bool whole) {
             float y[kPer];
-            exponents<T, true>(w, k, q);
 #pragma unroll
             for (int e = 0; e < kPer / 2; ++e)
                 halves(mul2(ex2_pair(q[e]), fma2(pair_of(k1, k1), q[e], pair_of(k0, k0))),
                        y[2 * e], y[2 * e + 1]);
-            store_vector<T>(out + (size_t)i * kPer, wide, y);
-        });
+            store_vector<T>(out + (size_t)i * kPer, whole, y);
+        };
+        if (fast)
+            each_vector<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
+                Pair q[kPer / 2];
+                exponents<T, true, false>(w, k, q);
+                put(i, q, true);
+            });
+        else
+            each_in_turn<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
+                Pair q[kPer / 2];
+                exponents<T, true, true>(w, k, q);
+                put(i, q, wide);
+            });
         auto one = [&](float x) {
             const float e = exponent(x, st.m, c2);
             return ex2(e) * fmaf(c1, e, c0);
