@@ -88,15 +88,30 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "r"(kFull));
-    return r;
+// A group of TH threads: half a warp, a warp or a CTA. Its lanes are those of a warp that work
+// together: 16 of half a warp, else 32.
+template <int TH>
+__host__ __device__ constexpr int lanes_of() { return TH < 32 ? TH : 32; }
+template <int TH>
+__device__ __forceinline__ unsigned lane_mask() {
+    return TH < 32 ? ((1u << (TH & 31)) - 1u) << (threadIdx.x & 31 & ~(TH - 1)) : kFull;
 }
-template <typename V>
-__device__ __forceinline__ V warp_sum(V v) {
+template <int TH>
+__device__ __forceinline__ float lanes_max(float v) {
+    if constexpr (TH < 32) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+        for (int o = TH / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(lane_mask<TH>(), v, o));
+        return v;
+    } else {
+        float r;
+        asm volatile("redux.sync.max.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "r"(kFull));
+        return r;
+    }
+}
+template <int TH, typename V>
+__device__ __forceinline__ V lanes_sum(V v) {
+#pragma unroll
+    for (int o = lanes_of<TH>() / 2; o; o >>= 1) v += __shfl_xor_sync(lane_mask<TH>(), v, o);
     return v;
 }
 
@@ -378,7 +393,7 @@ __device__ __forceinline__ Stats pass(const uint4* buf, int nv, int tid, float e
         });
         top = fmaxf(edge, fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a)));
     }
-    Stats st{warp_max(top), 0.f, 0.f};
+    Stats st{lanes_max<TH>(top), 0.f, 0.f};
     const Scale k(c2, st.m);
     Pair s2 = 0, w2 = 0;  // (0, 0)
     auto add = [&](const Pair (&t)[Elem<T>::kPer / 2]) {
@@ -418,16 +433,16 @@ __device__ __forceinline__ Stats pass(const uint4* buf, int nv, int tid, float e
 // The triples of up to 32 lanes as one (the same in every lane).
 template <bool kW>
 __device__ __forceinline__ Stats join_lanes(float m, float s, float w, float c2) {
-    const float M = warp_max(m);
+    const float M = lanes_max<32>(m);
     const float t = exponent(m, M, c2), f = ex2(t);
-    Stats r{M, warp_sum(f * s), 0.f};
-    if constexpr (kW) r.w = warp_sum(f * fmaf(s, t, w));
+    Stats r{M, lanes_sum<32>(f * s), 0.f};
+    if constexpr (kW) r.w = lanes_sum<32>(f * fmaf(s, t, w));
     return r;
 }
 
 template <int TH>
 __device__ __forceinline__ void group_sync() {
-    if constexpr (TH == 32) __syncwarp();
+    if constexpr (TH <= 32) __syncwarp(lane_mask<TH>());
     else __syncthreads();
 }
 
@@ -451,7 +466,7 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long
 // rows: a warp or CTA may leave its next row's triple while another still reads this row's.
 template <int TH>
 struct Joint {
-    float warp[2][3][TH / 32];
+    float warp[2][3][(TH + 31) / 32];
     float cta[2][3][kMaxCluster];
 };
 
@@ -459,14 +474,14 @@ struct Joint {
 // may leave what the others need after it in shared memory).
 template <int TH, bool kW>
 __device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, int parity, float c2) {
-    st.s = warp_sum(st.s);
-    if constexpr (kW) st.w = warp_sum(st.w);
-    if constexpr (TH == 32) {
+    st.s = lanes_sum<TH>(st.s);
+    if constexpr (kW) st.w = lanes_sum<TH>(st.w);
+    if constexpr (TH <= 32) {
         group_sync<TH>();
         return st;
     } else {
         const int lane = tid & 31;
-        float(&at)[3][TH / 32] = j.warp[parity];
+        float(&at)[3][(TH + 31) / 32] = j.warp[parity];
         if (lane == 0) {
             at[0][tid / 32] = st.m;
             at[1][tid / 32] = st.s;
@@ -511,15 +526,21 @@ __device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int c
     return st;
 }
 
+// Threads of a CTA: groups of short rows share one.
 template <int TH>
-__host__ __device__ constexpr int block_of() { return TH == 32 ? 256 : TH; }  // warps of short rows share a CTA
+__host__ __device__ constexpr int block_of() { return TH > 128 ? TH : 128; }
 // CTAs per SM a kernel is compiled for: 64 registers a thread
 template <int TH>
 __host__ __device__ constexpr int blocks_of() { return 1024 / block_of<TH>(); }
+// A thread's number in its group, and its group's in the CTA.
+template <int TH>
+__device__ __forceinline__ int thread_in_group() { return TH < block_of<TH>() ? threadIdx.x % TH : threadIdx.x; }
+template <int TH>
+__device__ __forceinline__ int group_in_block() { return TH < block_of<TH>() ? threadIdx.x / TH : 0; }
 
 // ------------------------------------------------------------------ host side
 
-constexpr int kWarpBytes = 8192;            // longest row of a warp
+constexpr int kShortBytes = 8192;           // longest row of half a warp or a warp
 constexpr int kPartBytes = 72 * 1024;       // a CTA's share that leaves room for three on a SM
 constexpr int kSmemBytes = 227 * 1024;
 
@@ -527,12 +548,12 @@ struct Shape {
     int threads, log_cluster;
 };
 
-// Threads and CTAs for a row of V elements: a warp up to 8 KB; else a CTA whose threads have at
+// Threads and CTAs for a row of V elements: `few` threads up to 8 KB; else a CTA whose threads have at
 // most about 64 KB / 256 = 256 bytes each; rows over 72 KB, and rows of a batch that would leave
 // SMs idle, are split over a cluster of up to 8 CTAs.
-inline Shape shape_of(int64_t rows, int V, int size, bool warp_ok) {
+inline Shape shape_of(int64_t rows, int V, int size, int few) {
     const int64_t bytes = (int64_t)V * size;
-    if (warp_ok && bytes <= kWarpBytes) return {32, 0};
+    if (few && bytes <= kShortBytes) return {few, 0};
     int lc = 0;
     while (lc < 3 && (bytes >> lc) > kPartBytes) ++lc;
     while (lc < 3 && (rows << (lc + 1)) <= 148 && (bytes >> (lc + 1)) >= 4096) ++lc;

@@ -35,14 +35,17 @@ struct TeacherIn {
     unsigned long long* n_bad;
 };
 
-constexpr int kLane = kMaxTop / 32;  // list entries of a lane
+// A place of the list: kept by the group's first lanes (16 or 32), lane l having places l,
+// l + lanes, ...
+struct alignas(16) Entry {
+    int id;          // -1: an empty place
+    float q, lq, x;  // weight, its logarithm, the student's logit
+};
 
-// The list, kept by the group's first warp, and what it leaves for the group. Entries of lane l:
-// l, l + 32, ...
+// What the list leaves for the group.
+template <typename T>
 struct ListShared {
-    int id[kMaxTop];  // -1: an empty place
-    float q[kMaxTop], lq[kMaxTop], x[kMaxTop];  // weight, its logarithm, the student's logit
-    float edge[16];   // the elements beside the row's vectors
+    T edge[16];       // the elements beside the row's vectors
     float m, s;       // this share's listed logits
     float Q, tail_q;  // sum of the weights (renormalised: 1), 1 - it where the tail is a class
     int empty;        // no entry, or none with weight
@@ -53,48 +56,29 @@ struct ListJoint {
     float cta[2][2][kMaxCluster];
 };
 
-// An element's bits, in the buffer or (as float32) beside it.
+// The bits of an element in shared memory.
 template <typename T>
-struct Cell {
-    using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
-    Bits* in;
-    float* beside;
-    __device__ __forceinline__ Cell(uint4* buf, float* edge, const Part<T>& p, int id)
-        : in(reinterpret_cast<Bits*>(buf) + p.place(id)),
-          beside(p.in_edges(id) ? edge + p.edge_lane(id) : nullptr) {}
-    __device__ __forceinline__ float value() const {
-        if (beside) return *beside;
-        if constexpr (sizeof(T) == 4) return __uint_as_float(*in);
-        else return __uint_as_float((uint32_t)*in << 16);
-    }
-    __device__ __forceinline__ void mark(int e) const {
-        if (beside) *beside = (float)e;
-        else *in = (Bits)e;
-    }
-    __device__ __forceinline__ bool marked(int e) const {
-        return beside ? *beside == (float)e : *in == (Bits)e;
-    }
-    __device__ __forceinline__ void hide() const {
-        if (beside) *beside = -kInf;
-        else *in = (Bits)Elem<T>::kFill;
-    }
-};
+using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
 
 template <typename T, int TH, bool kGrad>
 __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(RowsIn in, TeacherIn te) {
     constexpr int kRows = block_of<TH>() / TH, kPer = Part<T>::kPer;
-    extern __shared__ uint4 buffers[];  // [groups][slots]
+    extern __shared__ uint4 buffers[];  // [groups][slots]: the row's vectors, then the list
     __shared__ Joint<TH> joint[kRows];
-    __shared__ ListShared lists[kRows];
+    __shared__ ListShared<T> lists[kRows];
     __shared__ ListJoint listed_of;
-    const int tid = TH == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int group = TH == 32 ? threadIdx.x / 32 : 0;
-    const int lc = TH == 32 ? 0 : in.log_cluster, cluster = 1 << lc;
+    const int tid = thread_in_group<TH>();
+    const int group = group_in_block<TH>();
+    const int lc = TH <= 32 ? 0 : in.log_cluster, cluster = 1 << lc;
     const int rank = lc ? (int)cluster_ctarank() : 0;
-    const bool first_warp = rank == 0 && tid < 32;  // has the row's edges
+    const bool first_lanes = rank == 0 && tid < lanes_of<TH>();  // have the row's edges
     uint4* buf = buffers + (size_t)group * in.slots;
+    Entry* list = reinterpret_cast<Entry*>(buf + in.slots - te.k);
     const float c2 = in.c * kLog2e;
-    ListShared& ls = lists[group];
+    ListShared<T>& ls = lists[group];
+    constexpr int L = lanes_of<TH>(), kLane = kMaxTop / L;
+    const unsigned mask = lane_mask<TH>();
+    const bool lister = tid < L;
     if (lc) cluster_sync();  // every CTA runs before one writes to another
     RowWalk row((int64_t)(blockIdx.x >> lc) * kRows + group,
                 (int64_t)(gridDim.x >> lc) * kRows, in.n);
@@ -105,13 +89,13 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
     auto list_at = [&]() {
         if (row.r >= in.rows) return;
         if (kGrad && te.g != nullptr) g_next = __ldg(te.g + row.r);
-        if (tid < 32) {
+        if (lister) {
             const int64_t at = row.r * te.k;
 #pragma unroll
             for (int i = 0; i < kLane; ++i) {
-                const int e = tid + 32 * i;
+                if (i * L >= te.k) break;
+                const int e = tid + L * i;
                 id_next[i] = -1;
-                t_next[i] = -kInf;
                 if (e < te.k) {
                     id_next[i] = __ldg(te.ids + at + e);
                     t_next[i] = te.t_bf16 ? widen(__ldg(static_cast<const __nv_bfloat16*>(te.t) + at + e))
@@ -129,7 +113,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
         T* out = d + p.first;
         const float g = kGrad ? g_next : 1.f;
         const bool skip = kGrad && g == 0.f && te.loss == nullptr;  // zeros, whatever the row is
-        const int ie = first_warp ? p.edge(tid) : -1;
+        const int ie = first_lanes ? p.edge(tid) : -1;
         float edge = -kInf;
         if (!skip) {
             fetch<TH>(buf, p, tid);
@@ -138,23 +122,21 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
         int n = 0, bad = 0;
         float tmax = -kInf;
         bool broken = false;  // NaN or +inf among the entries
-        if (tid < 32) {
+        if (lister) {
 #pragma unroll
             for (int i = 0; i < kLane; ++i) {
-                const int e = tid + 32 * i;
+                if (i * L >= te.k) break;
+                const int e = tid + L * i;
+                if (e >= te.k) continue;
                 int id = id_next[i];
-                if (id >= in.V) {
-                    ++bad;
-                    id = -1;
-                }
+                if (id >= in.V) ++bad;
+                if (id < 0 || id >= in.V) id = -1;
                 const float t = id >= 0 ? t_next[i] : -kInf;
                 n += id >= 0;
                 tmax = fmaxf(tmax, t);
                 broken |= !(t < kInf);
-                if (e < te.k) {
-                    ls.id[e] = id < 0 ? -1 : id;
-                    ls.lq[e] = t;
-                }
+                list[e].id = id;
+                list[e].lq = t;
             }
             if (bad && rank == 0 && te.n_bad != nullptr)
                 atomicAdd(te.n_bad, (unsigned long long)bad);
@@ -162,43 +144,50 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
         row.next(in.n);
         list_at();
         bool empty = true;
-        unsigned first = 0;  // bit i: entry tid + 32 i is this share's, the first of its id
+        unsigned first = 0;  // bit i: entry tid + L i is this share's, the first of its id
         bool twice = false;  // some id is listed twice
         if (!skip) {
             arrived();
-            if (tid < 16) ls.edge[tid] = edge;
+            if (first_lanes && tid < 16 && ie >= 0) narrow(edge, &ls.edge[tid]);
             group_sync<TH>();  // the row is here
-            if (tid < 32) {
-                n = (int)__reduce_add_sync(kFull, (unsigned)n);
-                tmax = warp_max(tmax);
-                broken = __any_sync(kFull, broken);
-                for (int e = tid, i = 0; e < te.k; e += 32, ++i) {
-                    const int id = ls.id[e];
+            if (lister) {
+                using B = Bits<T>;
+                // where a listed element of this share is
+                auto cell = [&](int id) {
+                    const int q = p.place(id);
+                    return q >= 0 ? reinterpret_cast<B*>(buf) + q
+                                  : reinterpret_cast<B*>(ls.edge) + p.edge_lane(id);
+                };
+                for (int e = tid, i = 0; e < te.k; e += L, ++i) {
+                    const int id = list[e].id;
                     if (id < 0) continue;
                     if (p.place(id) >= 0 || (rank == 0 && p.in_edges(id))) {
                         first |= 1u << i;
-                        ls.x[e] = Cell<T>(buf, ls.edge, p, id).value();
+                        list[e].x = widen(*reinterpret_cast<const T*>(cell(id)));
                     } else if (rank == 0) {
-                        ls.x[e] = widen(p.x[id]);  // another CTA's; for the loss
+                        list[e].x = widen(p.x[id]);  // another CTA's; for the loss
                     }
                 }
-                __syncwarp();
+                __syncwarp(mask);
                 auto each_first = [&](auto&& f) {
-                    for (int e = tid, i = 0; e < te.k; e += 32, ++i)
+                    for (int e = tid, i = 0; e < te.k; e += L, ++i)
                         if ((first >> i) & 1u) f(e, i);
-                    __syncwarp();
+                    __syncwarp(mask);
                 };
-                each_first([&](int e, int) { Cell<T>(buf, ls.edge, p, ls.id[e]).mark(e); });
-                each_first([&](int e, int) { twice |= !Cell<T>(buf, ls.edge, p, ls.id[e]).marked(e); });
-                each_first([&](int e, int) { Cell<T>(buf, ls.edge, p, ls.id[e]).hide(); });
-                twice = __any_sync(kFull, twice);
+                each_first([&](int e, int) { *cell(list[e].id) = (B)e; });
+                each_first([&](int e, int) { twice |= *cell(list[e].id) != (B)e; });
+                each_first([&](int e, int) { *cell(list[e].id) = (B)Elem<T>::kFill; });
+                twice = __any_sync(mask, twice);
                 if (twice)  // the first of equal ids stands for all
                     each_first([&](int e, int i) {
                         for (int l = 0; l < e; ++l)
-                            if (ls.id[l] == ls.id[e]) first &= ~(1u << i);
+                            if (list[l].id == list[e].id) first &= ~(1u << i);
                     });
-                if (tid == 0) ls.empty = n == 0 || (!te.tail && tmax == -kInf && !broken);
-                if (tid < 16) edge = ls.edge[tid];
+                const bool some = __any_sync(mask, n > 0);
+                tmax = lanes_max<TH>(tmax);
+                broken = __any_sync(mask, broken);
+                if (tid == 0) ls.empty = !some || (!te.tail && tmax == -kInf && !broken);
+                if (ie >= 0) edge = widen(ls.edge[tid]);
             }
             group_sync<TH>();  // the listed tokens are hidden
             empty = ls.empty != 0;
@@ -207,41 +196,41 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
         if (!empty) {
             float top;
             rest = pass<TH, false, T>(buf, p.nv, tid, edge, c2, top);
-            if (tid < 32) {  // the weights and this share's listed logits
+            if (lister) {  // the weights and this share's listed logits
                 float Q = 1.f, tail_q = 0.f;
                 if (te.tail) {
                     // the tail's weight is what the list leaves of 1: in float64, or a tail of
                     // 1e-6 would be rounding
                     double sum = 0.0;
-                    for (int e = tid; e < te.k; e += 32) {
-                        const bool in_list = ls.id[e] >= 0;
-                        ls.q[e] = in_list ? expf(ls.lq[e]) : 0.f;
-                        if (in_list) sum += exp((double)ls.lq[e]);
+                    for (int e = tid; e < te.k; e += L) {
+                        const bool in_list = list[e].id >= 0;
+                        list[e].q = in_list ? expf(list[e].lq) : 0.f;
+                        if (in_list) sum += exp((double)list[e].lq);
                     }
-                    sum = warp_sum(sum);
+                    sum = lanes_sum<TH>(sum);
                     Q = broken ? NAN : (float)sum;
                     tail_q = (float)fmax(0.0, 1.0 - sum);
                 } else {
                     const float tm = tmax == -kInf ? 0.f : tmax;
                     float sum = 0.f;
-                    for (int e = tid; e < te.k; e += 32)
-                        if (ls.id[e] >= 0) sum += expf(ls.lq[e] - tm);
-                    sum = warp_sum(sum);
+                    for (int e = tid; e < te.k; e += L)
+                        if (list[e].id >= 0) sum += expf(list[e].lq - tm);
+                    sum = lanes_sum<TH>(sum);
                     if (broken) Q = NAN;
                     const float ln_sum = logf(sum);
-                    for (int e = tid; e < te.k; e += 32) {
-                        const float lq = (ls.lq[e] - tm) - ln_sum;
-                        ls.lq[e] = lq;
-                        ls.q[e] = ls.id[e] >= 0 ? expf(lq) : 0.f;
+                    for (int e = tid; e < te.k; e += L) {
+                        const float lq = (list[e].lq - tm) - ln_sum;
+                        list[e].lq = lq;
+                        list[e].q = list[e].id >= 0 ? expf(lq) : 0.f;
                     }
                 }
                 float m = -kInf, sum = 0.f;
-                for (int e = tid, i = 0; e < te.k; e += 32, ++i)
-                    if ((first >> i) & 1u) m = fmaxf(m, ls.x[e]);
-                m = warp_max(m);
-                for (int e = tid, i = 0; e < te.k; e += 32, ++i)
-                    if ((first >> i) & 1u) sum += ex2(exponent(ls.x[e], m, c2));
-                sum = warp_sum(sum);
+                for (int e = tid, i = 0; e < te.k; e += L, ++i)
+                    if ((first >> i) & 1u) m = fmaxf(m, list[e].x);
+                m = lanes_max<TH>(m);
+                for (int e = tid, i = 0; e < te.k; e += L, ++i)
+                    if ((first >> i) & 1u) sum += ex2(exponent(list[e].x, m, c2));
+                sum = lanes_sum<TH>(sum);
                 if (tid == 0) {
                     ls.m = m;
                     ls.s = sum;
@@ -276,14 +265,14 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
             qr = rest.s == 0.f ? 0.f : ls.tail_q;
             Q = te.tail ? ls.Q + qr : ls.Q;
         }
-        if (te.loss != nullptr && first_warp) {
+        if (te.loss != nullptr && first_lanes) {
             const float ln_s = ln(all.s);
             float part = 0.f;
             if (!empty) {
-                for (int e = tid; e < te.k; e += 32)
-                    if (ls.id[e] >= 0 && ls.q[e] != 0.f)
-                        part += ls.q[e] * (ls.lq[e] - (all.s == 0.f ? -kInf : log_prob(ls.x[e], in.c, all.m, ln_s)));
-                part = warp_sum(part);
+                for (int e = tid; e < te.k; e += L)
+                    if (list[e].id >= 0 && list[e].q != 0.f)
+                        part += list[e].q * (list[e].lq - (all.s == 0.f ? -kInf : log_prob(list[e].x, in.c, all.m, ln_s)));
+                part = lanes_sum<TH>(part);
                 if (qr > 0.f)
                     part += qr * (logf(qr) - (in.c * (rest.m - all.m) + ln(rest.s) - ln_s));
             }
@@ -325,17 +314,17 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
                     });
                 if (ie >= 0) narrow(ex2(exponent(edge, rest.m, c2)) * f0, d + ie);
                 group_sync<TH>();  // the listed tokens' places hold the rest's gradient by now
-                if (tid < 32)
-                    for (int e = tid, i = 0; e < te.k; e += 32, ++i)
+                if (lister)
+                    for (int e = tid, i = 0; e < te.k; e += L, ++i)
                         if ((first >> i) & 1u) {
-                            const int id = ls.id[e];
-                            float w = ls.q[e];
+                            const int id = list[e].id;
+                            float w = list[e].q;
                             if (twice) {
                                 w = 0.f;
                                 for (int l = 0; l < te.k; ++l)
-                                    if (ls.id[l] == id) w += ls.q[l];
+                                    if (list[l].id == id) w += list[l].q;
                             }
-                            const float pi = ex2(exponent(ls.x[e], all.m, c2)) * inv;
+                            const float pi = ex2(exponent(list[e].x, all.m, c2)) * inv;
                             narrow(gc * (Q * pi - w), d + id);
                         }
             }
@@ -347,9 +336,9 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
 template <typename T, bool kGrad>
 cudaError_t distill_of(int threads, const RowsIn& in, const TeacherIn& te, cudaStream_t s) {
     switch (threads) {
-        case 32: return launch_rows<&k_distill<T, 32, kGrad>, 32>(in, 18 * 1024, s, in, te);
-        case 128: return launch_rows<&k_distill<T, 128, kGrad>, 128>(in, 4096, s, in, te);
-        default: return launch_rows<&k_distill<T, 256, kGrad>, 256>(in, 4096, s, in, te);
+        case 16: return launch_rows<&k_distill<T, 16, kGrad>, 16>(in, 1024, s, in, te);
+        case 128: return launch_rows<&k_distill<T, 128, kGrad>, 128>(in, 1024, s, in, te);
+        default: return launch_rows<&k_distill<T, 256, kGrad>, 256>(in, 1024, s, in, te);
     }
 }
 
@@ -377,9 +366,9 @@ int distill(const void* logits, int dtype, int64_t S, int n, int V, int64_t stri
                  !apart_or_same(logits, stride_s, stride_n, dlogits, d_stride_s, d_stride_n, S, n,
                                 V, size)))
         return MIMI_RVQ_EINVAL;
-    const Shape sh = shape_of(S * n, V, size, true);
+    const Shape sh = shape_of(S * n, V, size, 16);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
-                    slots_of(V, size, sh.log_cluster)};
+                    slots_of(V, size, sh.log_cluster) + k};
     const TeacherIn te{ids, teacher, teacher_dtype == MIMI_RVQ_BF16, k, tail, g, loss, dlogits,
                        d_stride_s, d_stride_n, reinterpret_cast<unsigned long long*>(n_bad)};
     if (dtype == MIMI_RVQ_BF16)

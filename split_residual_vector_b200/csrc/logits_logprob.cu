@@ -259,9 +259,9 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
     __shared__ Joint<TH> joint[kRows];
     __shared__ TopShared<kTop ? TH : 32> tops[kTop ? kRows : 1];
     __shared__ TopLists<kTop ? TH : 32> lists;
-    const int tid = TH == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int group = TH == 32 ? threadIdx.x / 32 : 0;
-    const int lc = TH == 32 ? 0 : in.log_cluster, cluster = 1 << lc;
+    const int tid = thread_in_group<TH>();
+    const int group = group_in_block<TH>();
+    const int lc = TH <= 32 ? 0 : in.log_cluster, cluster = 1 << lc;
     const int rank = lc ? (int)cluster_ctarank() : 0;
     const bool first_warp = rank == 0 && tid < 32;  // has the row's edges
     uint4* buf = buffers + (size_t)group * in.slots;
@@ -375,9 +375,9 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
     constexpr int kRows = block_of<TH>() / TH, kPer = Part<T>::kPer;
     extern __shared__ uint4 buffers[];  // [groups][slots]
     __shared__ Joint<TH> joint[kRows];
-    const int tid = TH == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int group = TH == 32 ? threadIdx.x / 32 : 0;
-    const int lc = TH == 32 ? 0 : in.log_cluster, cluster = 1 << lc;
+    const int tid = thread_in_group<TH>();
+    const int group = group_in_block<TH>();
+    const int lc = TH <= 32 ? 0 : in.log_cluster, cluster = 1 << lc;
     const int rank = lc ? (int)cluster_ctarank() : 0;
     const bool first_warp = rank == 0 && tid < 32;
     uint4* buf = buffers + (size_t)group * in.slots;
@@ -481,9 +481,10 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
 template <typename T, bool kTop>
 cudaError_t forward_of(int threads, const RowsIn& in, const TokensIn& tk, const ValuesOut& o,
                        cudaStream_t s) {
+    constexpr int kShort = kTop ? 32 : 16;
     constexpr int kLists = kTop ? 18 * 1024 : 1024;  // static shared memory, rounded up
     switch (threads) {
-        case 32: return launch_rows<&k_logprob<T, 32, kTop>, 32>(in, kTop ? 10 * 1024 : 512, s, in, tk, o);
+        case kShort: return launch_rows<&k_logprob<T, kShort, kTop>, kShort>(in, kTop ? 5 * 1024 : 512, s, in, tk, o);
         case 128: return launch_rows<&k_logprob<T, 128, kTop>, 128>(in, kLists, s, in, tk, o);
         default: return launch_rows<&k_logprob<T, 256, kTop>, 256>(in, kLists, s, in, tk, o);
     }
@@ -493,7 +494,7 @@ template <typename T>
 cudaError_t gradient_of(int threads, const RowsIn& in, const TokensIn& tk, const GradIn& g,
                         const ValuesOut& o, cudaStream_t s) {
     switch (threads) {
-        case 32: return launch_rows<&k_logprob_grad<T, 32>, 32>(in, 4096, s, in, tk, g, o);
+        case 16: return launch_rows<&k_logprob_grad<T, 16>, 16>(in, 1024, s, in, tk, g, o);
         case 128: return launch_rows<&k_logprob_grad<T, 128>, 128>(in, 1024, s, in, tk, g, o);
         default: return launch_rows<&k_logprob_grad<T, 256>, 256>(in, 1024, s, in, tk, g, o);
     }
@@ -523,7 +524,7 @@ extern "C" int mimi_rvq_token_logprob(const void* logits, int dtype, int64_t S, 
     if (top_k > 0 && (!maybe_on_device(top_ids, 4, dev) || !maybe_on_device(top_logprob, 4, dev)))
         return MIMI_RVQ_EINVAL;
     const int k = top_ids != nullptr || top_logprob != nullptr ? top_k : 0;
-    const Shape sh = shape_of(S * n, V, size, k <= kWarpTop);
+    const Shape sh = shape_of(S * n, V, size, k == 0 ? 16 : k <= kWarpTop ? 32 : 0);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
                     slots_of(V, size, sh.log_cluster)};
     const TokensIn tk{tokens, tok_stride_s, tok_stride_n, pad,
@@ -559,7 +560,7 @@ extern "C" int mimi_rvq_token_logprob_grad(
         !maybe_on_device(logprob, 4, dev) || !maybe_on_device(entropy, 4, dev) ||
         !maybe_on_device(lse, 4, dev) || !maybe_on_device(n_bad, 8, dev))
         return MIMI_RVQ_EINVAL;
-    const Shape sh = shape_of(S * n, V, size, true);
+    const Shape sh = shape_of(S * n, V, size, 16);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
                     slots_of(V, size, sh.log_cluster)};
     const TokensIn tk{tokens, tok_stride_s, tok_stride_n, pad,
