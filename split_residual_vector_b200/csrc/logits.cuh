@@ -548,14 +548,14 @@ struct Shape {
     int threads, log_cluster;
 };
 
-// Threads and CTAs for a row of V elements: `few` threads up to 8 KB; else a CTA whose threads have at
-// most about 64 KB / 256 = 256 bytes each; rows over 72 KB, and rows of a batch that would leave
+// Threads and CTAs for a row of V elements: `few` threads up to 8 KB; else a CTA of 128 or 256.
+// Rows over 72 KB that have to lie in shared memory whole, and rows of a batch that would leave
 // SMs idle, are split over a cluster of up to 8 CTAs.
-inline Shape shape_of(int64_t rows, int V, int size, int few) {
+inline Shape shape_of(int64_t rows, int V, int size, int few, bool whole) {
     const int64_t bytes = (int64_t)V * size;
     if (few && bytes <= kShortBytes) return {few, 0};
     int lc = 0;
-    while (lc < 3 && (bytes >> lc) > kPartBytes) ++lc;
+    while (whole && lc < 3 && (bytes >> lc) > kPartBytes) ++lc;
     while (lc < 3 && (rows << (lc + 1)) <= 148 && (bytes >> (lc + 1)) >= 4096) ++lc;
     return {(bytes >> lc) <= 16384 ? 128 : 256, lc};
 }

@@ -366,7 +366,7 @@ int distill(const void* logits, int dtype, int64_t S, int n, int V, int64_t stri
                  !apart_or_same(logits, stride_s, stride_n, dlogits, d_stride_s, d_stride_n, S, n,
                                 V, size)))
         return MIMI_RVQ_EINVAL;
-    const Shape sh = shape_of(S * n, V, size, 16);
+    const Shape sh = shape_of(S * n, V, size, 16, true);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
                     slots_of(V, size, sh.log_cluster) + k};
     const TeacherIn te{ids, teacher, teacher_dtype == MIMI_RVQ_BF16, k, tail, g, loss, dlogits,

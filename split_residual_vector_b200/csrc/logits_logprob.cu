@@ -3,7 +3,10 @@
 // include/mimi_rvq_streams.h; layout and statistics in logits.cuh.
 //
 // Forward: one pass over the row, bound by reading it (2 or 4 bytes a logit for
-// one exponential, two sums and a maximum).
+// one exponential, two sums and a maximum). Short rows lie in shared memory
+// whole; a longer one passes through a ring of chunks in the order of reading,
+// which runs on into the CTA's next row while this one's sums are joined and its
+// alternatives ordered, with a running maximum a warp.
 //
 // Alternatives: the k largest by (logit descending, id ascending). A bound that
 // at least k logits reach costs almost nothing on top of the pass: every
@@ -99,31 +102,18 @@ constexpr int kWarpTop = 24;
 
 template <int TH>
 struct TopShared {
-    static constexpr int kGroups = TH > 256 ? 256 : TH;  // maxima that bound the k-th logit
-    static constexpr int kCap = TH == 32 ? 128 : 1024;
-    uint32_t most[TH == 32 ? 1 : kGroups];
+    static constexpr int kCap = TH == 32 ? 128 : 512;
+    uint32_t most[TH == 32 ? 1 : TH];  // the threads' maxima
     float bound;
     int count;
     alignas(16) Key list[kCap + 8];
     Key last[TH / 32];
 };
-template <int TH>
-struct TopLists {  // the keys that a cluster's CTAs give its first one
-    Key of[TH == 32 ? 1 : kMaxCluster][TH == 32 ? 1 : kMaxTop];
+// The keys that a cluster's CTAs give its first one.
+struct TopLists {
+    Key of[kMaxCluster][kMaxTop];
     int count[kMaxCluster];
 };
-
-// Leaves the groups' maxima; the group's barrier follows.
-template <int TH>
-__device__ __forceinline__ void leave_maxima(TopShared<TH>& sh, float top, int tid) {
-    constexpr int kShare = TH / TopShared<TH>::kGroups;
-    if constexpr (TH > 32) {
-        uint32_t g = order_of(top);
-#pragma unroll
-        for (int o = 1; o < kShare; o *= 2) g = max(g, __shfl_xor_sync(kFull, g, o));
-        if (tid % kShare == 0) sh.most[tid / kShare] = g;
-    }
-}
 
 // f(value, id) for this thread's logits of the share.
 template <int TH, typename T, typename F>
@@ -140,43 +130,48 @@ __device__ __forceinline__ void each_logit(const uint4* buf, const Part<T>& p, i
     if (edge > -kInf) f(edge, p.edge(tid));
 }
 
-// The share's logits that reach the bound, as unordered keys in sh.list: returns their number,
-// at least min(k, the logits above -inf); past kCap the list is not complete.
-template <int TH, typename T>
-__device__ __forceinline__ int collect(TopShared<TH>& sh, const Part<T>& p, const uint4* buf,
-                                       float edge, float top, int tid, int k) {
-    constexpr int kN = TopShared<TH>::kGroups / 32, kCap = TopShared<TH>::kCap;
-    if (tid < 32) {
-        uint32_t q[kN];
-        uint32_t hi = 0, lo = 0xFFFFFFFFu;
+// Leaves in sh.bound the largest bound (in steps of 2^16 of the values' order) that k of the
+// threads' maxima reach, or the lowest finite value; called by the first warp behind a barrier.
+template <int TH>
+__device__ __forceinline__ void find_bound(TopShared<TH>& sh, float top, int tid, int k) {
+    constexpr int kN = TH / 32;
+    uint32_t q[kN];
+    uint32_t hi = 0, lo = 0xFFFFFFFFu;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            q[i] = TH == 32 ? order_of(top) : sh.most[tid + 32 * i];
-            hi = max(hi, q[i]);
-            lo = min(lo, q[i]);
-        }
-        hi = __reduce_max_sync(kFull, hi);
-        lo = __reduce_min_sync(kFull, lo);
-        // the largest bound, in steps of 2^16, that k maxima reach: bits that all maxima share
-        // are theirs, and k maxima exactly is as good as it gets
-        uint32_t b = 0;
-        if (k <= 32 * kN) {
-            const int top_bit = 31 - __clz(lo ^ hi);  // -1: all are equal
-            b = lo == hi ? lo : lo & ~((2u << top_bit) - 1u);
-            for (int bit = top_bit; bit >= 16; --bit) {
-                const uint32_t t = b | (1u << bit);
-                int n = 0;
+    for (int i = 0; i < kN; ++i) {
+        q[i] = TH == 32 ? order_of(top) : sh.most[tid + 32 * i];
+        hi = max(hi, q[i]);
+        lo = min(lo, q[i]);
+    }
+    hi = __reduce_max_sync(kFull, hi);
+    lo = __reduce_min_sync(kFull, lo);
+    // bits that all maxima share are the bound's, and k maxima exactly is as good as it gets
+    uint32_t b = 0;
+    if (k <= TH) {
+        const int top_bit = 31 - __clz(lo ^ hi);  // -1: all are equal
+        b = lo == hi ? lo : lo & ~((2u << top_bit) - 1u);
+        for (int bit = top_bit; bit >= 16; --bit) {
+            const uint32_t t = b | (1u << bit);
+            int n = 0;
 #pragma unroll
-                for (int i = 0; i < kN; ++i) n += __popc(__ballot_sync(kFull, q[i] >= t));
-                if (n >= k) b = t;
-                if (n == k) break;
-            }
-        }
-        if (tid == 0) {
-            sh.bound = order_value(max(b, kOrderNegInf + 1));
-            sh.count = 0;
+            for (int i = 0; i < kN; ++i) n += __popc(__ballot_sync(kFull, q[i] >= t));
+            if (n >= k) b = t;
+            if (n == k) break;
         }
     }
+    if (tid == 0) {
+        sh.bound = order_value(max(b, kOrderNegInf + 1));
+        sh.count = 0;
+    }
+}
+
+// A warp's row: the logits that reach the bound, as unordered keys in sh.list; returns their
+// number, at least min(k, the logits above -inf); past kCap the list is not complete.
+template <typename T>
+__device__ __forceinline__ int collect(TopShared<32>& sh, const Part<T>& p, const uint4* buf,
+                                       float edge, float top, int tid, int k) {
+    constexpr int TH = 32, kCap = TopShared<32>::kCap;
+    find_bound(sh, top, tid, k);
     group_sync<TH>();
     const float bound = sh.bound;
     const int lane = tid & 31;
@@ -251,49 +246,94 @@ __device__ __noinline__ int take_rounds(TopShared<TH>& sh, const Part<T> p, cons
 
 // ------------------------------------------------------------------ forward
 
+// A row's alternatives from the n keys of sh.list, or (over: the list is not complete) by rounds
+// over the logits in `buf`.
+template <int TH, typename T>
+__device__ __forceinline__ void put_top(TopShared<TH>& sh, const ValuesOut& o, int64_t r, int n,
+                                        bool over, const Stats& st, float c, int tid,
+                                        const Part<T>& p, const uint4* buf, float edge) {
+    const bool broken = !(st.s < kInf);
+    const float ln_s = ln(st.s);
+    int32_t* const ids = o.top_ids == nullptr ? nullptr : o.top_ids + r * o.k;
+    float* const lps = o.top_logprob == nullptr ? nullptr : o.top_logprob + r * o.k;
+    const float m = st.m;
+    auto out = [=](int place, Key key) {
+        if (ids != nullptr) ids[place] = key ? key_id(key) : -1;
+        if (lps != nullptr)
+            lps[place] = broken ? NAN : key ? log_prob(key_value(key), c, m, ln_s) : -kInf;
+    };
+    if (broken) n = 0;
+    else if (over) n = take_rounds<TH>(sh, p, buf, edge, tid, o.k, out);
+    else order_list(sh, n, tid, o.k, out);
+    for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
+}
+
+// The same from the lists that the cluster's CTAs gave.
+template <int TH>
+__device__ __forceinline__ void put_cluster_top(TopShared<TH>& sh, const TopLists& lists,
+                                                int cluster, const ValuesOut& o, int64_t r,
+                                                const Stats& st, float c, int tid) {
+    const bool broken = !(st.s < kInf);
+    const float ln_s = ln(st.s), m = st.m;
+    int32_t* const ids = o.top_ids == nullptr ? nullptr : o.top_ids + r * o.k;
+    float* const lps = o.top_logprob == nullptr ? nullptr : o.top_logprob + r * o.k;
+    auto out = [=](int place, Key key) {
+        if (ids != nullptr) ids[place] = key ? key_id(key) : -1;
+        if (lps != nullptr)
+            lps[place] = broken ? NAN : key ? log_prob(key_value(key), c, m, ln_s) : -kInf;
+    };
+    int n = 0;
+    for (int l = 0; l < cluster && !broken; ++l) n += lists.count[l];
+    if (!broken)
+        for (int i = tid; i < n; i += TH) {
+            int l = 0, e = i;
+            while (e >= lists.count[l]) e -= lists.count[l++];
+            const Key key = lists.of[l][e];
+            int place = 0;
+            for (int l2 = 0; l2 < cluster; ++l2) {
+                const int m2 = lists.count[l2];
+                int e2 = 0;
+                for (; e2 + 4 <= m2; e2 += 4)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) place += lists.of[l2][e2 + q] > key;
+                for (; e2 < m2; ++e2) place += lists.of[l2][e2] > key;
+            }
+            if (place < o.k) out(place, key);
+        }
+    for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
+}
+
+// Rows of up to 8 KB, each in its group's shared memory: half a warp a row, or a warp where
+// alternatives are wanted.
 template <typename T, int TH, bool kTop>
 __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
     k_logprob(RowsIn in, TokensIn tk, ValuesOut o) {
+    static_assert(TH == 16 || TH == 32, "half a warp or a warp");
     constexpr int kRows = block_of<TH>() / TH;
     extern __shared__ uint4 buffers[];  // [groups][slots]
     __shared__ Joint<TH> joint[kRows];
-    __shared__ TopShared<kTop ? TH : 32> tops[kTop ? kRows : 1];
-    __shared__ TopLists<kTop ? TH : 32> lists;
+    __shared__ TopShared<32> tops[kTop ? kRows : 1];
     const int tid = thread_in_group<TH>();
     const int group = group_in_block<TH>();
-    const int lc = TH <= 32 ? 0 : in.log_cluster, cluster = 1 << lc;
-    const int rank = lc ? (int)cluster_ctarank() : 0;
-    const bool first_warp = rank == 0 && tid < 32;  // has the row's edges
     uint4* buf = buffers + (size_t)group * in.slots;
     const float c2 = in.c * kLog2e;
-    if (lc) cluster_arrive();  // every CTA runs before one writes to another
-    bool started = lc == 0;
-    RowWalk row((int64_t)(blockIdx.x >> lc) * kRows + group,
-                (int64_t)(gridDim.x >> lc) * kRows, in.n);
+    RowWalk row((int64_t)blockIdx.x * kRows + group, (int64_t)gridDim.x * kRows, in.n);
+    if (row.r >= in.rows) return;
     auto part_at = [&]() {
-        return Part<T>(static_cast<const T*>(in.x) + row.s * in.ss + row.j * in.sn, in.V, rank, lc);
+        return Part<T>(static_cast<const T*>(in.x) + row.s * in.ss + row.j * in.sn, in.V, 0, 0);
     };
     auto edge_of = [&](const Part<T>& p) {
-        const int i = first_warp ? p.edge(tid) : -1;
+        const int i = p.edge(tid);
         return i < 0 ? -kInf : widen(p.x[i]);
     };
-    if (row.r >= in.rows) {
-        if (!started) cluster_wait();
-        return;
-    }
     Part<T> p = part_at();
     fetch<TH>(buf, p, tid);
     float edge = edge_of(p);
-    const bool teller = first_warp && tid == 0;
-    int32_t token = teller ? token_at(tk, row, in.rows) : -1;
-    for (int parity = 0;; parity ^= 1) {
+    int32_t token = token_at(tk, row, in.rows);
+    while (true) {
         const int64_t r = row.r;
-        int t = -1;
-        float xt = 0.f;
-        if (teller) {
-            t = target_of(tk, token, in.V, true);
-            if (t >= 0) xt = widen(p.x[t]);
-        }
+        const int t = target_of(tk, token, in.V, tid == 0);
+        const float xt = t >= 0 ? widen(p.x[t]) : 0.f;
         arrived();
         float top;
         Stats st = pass<TH, true, T>(buf, p.nv, tid, edge, c2, top);
@@ -304,66 +344,252 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
             p = part_at();
             fetch<TH>(buf, p, tid);
             edge = edge_of(p);
-            if (teller) token = token_at(tk, row, in.rows);
+            token = token_at(tk, row, in.rows);
         };
-        if constexpr (kTop) leave_maxima<TH>(tops[group], top, tid);
-        else send_next();
-        st = join_group<TH, true>(joint[group], st, tid, parity, c2);
+        if constexpr (kTop) {
+            st = join_group<TH, true>(joint[group], st, tid, 0, c2);
+            const int n = collect(tops[group], p, buf, edge, top, tid, o.k);
+            const bool over = n > TopShared<32>::kCap;
+            if (tid == 0) put_values(o, r, t, xt, in.c, st);
+            const Part<T> here = p;
+            const float here_edge = edge;
+            if (!over) send_next();
+            put_top<TH>(tops[group], o, r, n, over, st, in.c, tid, here, buf, here_edge);
+            if (over) send_next();
+        } else {
+            send_next();
+            st = join_group<TH, true>(joint[group], st, tid, 0, c2);
+            if (tid == 0) put_values(o, r, t, xt, in.c, st);
+        }
+        if (!more) break;
+    }
+}
+
+// Longer rows: 128 threads a row, or the CTAs of a cluster where rows are few. A thread copies
+// and reads its own places of a ring of kStages chunks of kU vectors a thread; copies run
+// kStages - 1 chunks ahead, across rows.
+constexpr int kLong = 128, kU = 4, kStages = 3, kChunk = kU * kLong, kRemember = 16;
+
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kLong, blocks_of<kLong>())
+    k_logprob_long(RowsIn in, TokensIn tk, ValuesOut o) {
+    constexpr int TH = kLong, kPer = Elem<T>::kPer, kPairs = kPer / 2;
+    extern __shared__ uint4 ring[];  // [kStages][kU][TH], then TopLists in a cluster
+    __shared__ Joint<TH> joint;
+    __shared__ TopShared<kTop ? TH : 32> tops;
+    __shared__ float of_chunk[kTop ? kRemember : 1][TH];  // threads' maxima of chunks c, c + 16, ...
+    TopLists& lists = *reinterpret_cast<TopLists*>(ring + kStages * kChunk);
+    const int tid = threadIdx.x;
+    const int lc = in.log_cluster, cluster = 1 << lc;
+    const int rank = lc ? (int)cluster_ctarank() : 0;
+    const bool first_warp = rank == 0 && tid < 32;  // has the row's edges
+    const float c2 = in.c * kLog2e;
+    if (lc) cluster_arrive();  // every CTA runs before one writes to another
+    bool started = lc == 0;
+    RowWalk row(blockIdx.x >> lc, gridDim.x >> lc, in.n);
+    auto part_at = [&](const RowWalk& w) {
+        return Part<T>(static_cast<const T*>(in.x) + w.s * in.ss + w.j * in.sn, in.V, rank, lc);
+    };
+    auto chunks_of = [](const Part<T>& p) { return max(1, (p.nv + kChunk - 1) / kChunk); };
+    // copies, ahead of the chunk that is read; one group of copies per call
+    RowWalk ahead = row;
+    Part<T> to_come = part_at(ahead);
+    int next_chunk = 0, left_to_come = chunks_of(to_come), stage_in = 0, stage_out = 0;
+    auto send = [&]() {
+        if (ahead.r < in.rows) {
+            const int base = next_chunk * kChunk + tid;
+            const T* src = to_come.x + to_come.first + (size_t)base * kPer;
+            uint4* dst = ring + stage_in * kChunk + tid;
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (base + u * TH < to_come.nv) copy16(dst + u * TH, src + (size_t)u * TH * kPer);
+            ++next_chunk;
+            if (--left_to_come == 0) {
+                ahead.next(in.n);
+                if (ahead.r < in.rows) {
+                    to_come = part_at(ahead);
+                    left_to_come = chunks_of(to_come);
+                    next_chunk = 0;
+                }
+            }
+        }
+        stage_in = stage_in == kStages - 1 ? 0 : stage_in + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) send();
+    int32_t token = first_warp ? token_at(tk, row, in.rows) : -1;
+    for (int parity = 0; row.r < in.rows; parity ^= 1) {
+        const int64_t r = row.r;
+        const Part<T> p = part_at(row);
+        const int chunks = chunks_of(p);
+        const int t = first_warp ? target_of(tk, token, in.V, tid == 0) : -1;
+        const int ie = first_warp ? p.edge(tid) : -1;
+        const float edge = ie < 0 ? -kInf : widen(p.x[ie]);
+        const float xt = t >= 0 ? widen(p.x[t]) : 0.f;
+        row.next(in.n);
+        token = first_warp ? token_at(tk, row, in.rows) : -1;
+        float top = -kInf, m = -kInf;  // the thread's maximum, the warp's
+        Scale k(c2, m);
+        Pair s2 = 0, w2 = 0;  // (0, 0)
+        for (int c = 0; c < chunks; ++c) {
+            send();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            const uint4* at = ring + stage_out * kChunk + tid;
+            stage_out = stage_out == kStages - 1 ? 0 : stage_out + 1;
+            const int left = p.nv - c * kChunk;
+            uint32_t w[kU][4];
+            if (left >= kChunk) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const uint4 q = at[u * TH];
+                    w[u][0] = q.x, w[u][1] = q.y, w[u][2] = q.z, w[u][3] = q.w;
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    uint4 q = make_uint4(Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill);
+                    if (u * TH + tid < left) q = at[u * TH];
+                    w[u][0] = q.x, w[u][1] = q.y, w[u][2] = q.z, w[u][3] = q.w;
+                }
+            }
+            float mx;
+            if constexpr (sizeof(T) == 4) {
+                mx = vector_max<T>(w[0]);
+#pragma unroll
+                for (int u = 1; u < kU; ++u) mx = fmaxf(mx, vector_max<T>(w[u]));
+            } else {
+                uint32_t a = Elem<T>::kFill;
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    a = max_bf16x2(a, max_bf16x2(max_bf16x2(w[u][0], w[u][1]), max_bf16x2(w[u][2], w[u][3])));
+                mx = fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a));
+            }
+            if constexpr (kTop) {
+                float& of = of_chunk[c % kRemember][tid];
+                of = c < kRemember ? mx : fmaxf(of, mx);
+            }
+            if (c == chunks - 1) mx = fmaxf(mx, edge);
+            top = fmaxf(top, mx);
+            if (__any_sync(kFull, mx > m)) {  // a new maximum: the sums so far move to it
+                const float m_new = fmaxf(m, lanes_max<32>(mx));
+                const Scale k_new(c2, m_new);
+                float s, s1, w0, w1;
+                halves(s2, s, s1);
+                halves(w2, w0, w1);
+                s += s1;
+                const float back = ex2(-k.shift);
+                w0 = fmaf(-k.shift, s, w0 + w1) * back;
+                s *= back;
+                const float d = m == -kInf ? 0.f : exponent(m, m_new, c2) + k_new.shift;
+                const float f = ex2(d);
+                s2 = pair_of(s * f, 0.f);
+                w2 = pair_of(f * fmaf(s, d, w0), 0.f);
+                m = m_new;
+                k = k_new;
+            }
+            auto add = [&](const Pair (&q)[kPairs]) {
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    const Pair e = ex2_pair(q[j]);
+                    s2 = add2(s2, e);
+                    w2 = fma2(e, q[j], w2);
+                }
+            };
+            if (!k.far) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    Pair q[kPairs];
+                    exponents<T, true, false>(w[u], k, q);
+                    add(q);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    Pair q[kPairs];
+                    exponents<T, true, true>(w[u], k, q);
+                    add(q);
+                }
+            }
+        }
+        Stats st{m, 0.f, 0.f};
+        {
+            float s, s1, w0, w1;
+            halves(s2, s, s1);
+            halves(w2, w0, w1);
+            s += s1;
+            const float back = ex2(-k.shift), te = exponent(edge, m, c2), e = ex2(te);
+            st.s = fmaf(s, back, e);
+            st.w = fmaf(fmaf(-k.shift, s, w0 + w1), back, e * te);
+        }
+        if constexpr (kTop) tops.most[tid] = order_of(top);
+        st = join_group<TH, true>(joint, st, tid, parity, c2);
         int n = 0;
-        if constexpr (kTop) n = collect<TH>(tops[group], p, buf, edge, top, tid, o.k);
-        if (TH > 32 && lc) {  // the first CTA gets the others' triples and keys
+        const uint4* vectors = reinterpret_cast<const uint4*>(p.x + p.first);
+        if constexpr (kTop) {
+            if (tid < 32) find_bound(tops, top, tid, o.k);
+            __syncthreads();
+            const float bound = tops.bound;
+            if (top >= bound) {  // its logits that reach it, from the chunks whose maximum does
+                auto keep = [&](float x, int id) {
+                    if (x < bound) return;
+                    const int at = atomicAdd(&tops.count, 1);
+                    if (at < TopShared<TH>::kCap) tops.list[at] = key_of(x, id);
+                };
+                for (int c = 0; c < chunks; ++c) {
+                    if (of_chunk[c % kRemember][tid] < bound) continue;
+                    uint4 q[kU];
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        const int i = c * kChunk + u * TH + tid;
+                        q[u] = make_uint4(Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill);
+                        if (i < p.nv) q[u] = vectors[i];
+                    }
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                        if (vector_max<T>(w) < bound) continue;
+                        const int id = p.first + (c * kChunk + u * TH + tid) * kPer;
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j) keep(element<T>(w, j), id + j);
+                    }
+                }
+                if (ie >= 0) keep(edge, ie);
+            }
+            __syncthreads();
+            n = tops.count;
+        }
+        if (lc) {  // the first CTA gets the others' triples and keys
             if (!started) cluster_wait();
             started = true;
-            if (tid == 0) push_stats<TH, true>(joint[0], st, rank, 0, 0);
+            if (tid == 0) push_stats<TH, true>(joint, st, rank, 0, 0);
             if constexpr (kTop) {
                 const uint32_t to = cluster_map(smem_u32(&lists.of[rank][0]), 0);
                 auto give = [to](int place, Key key) { st_cluster_u64(to + 8 * place, key); };
                 if (n > TopShared<TH>::kCap) {
-                    n = take_rounds<TH>(tops[0], p, buf, edge, tid, o.k, give);
-                } else if (n > kMaxTop) {
-                    order_list(tops[0], n, tid, o.k, give);
+                    n = take_rounds<TH>(tops, p, vectors, edge, tid, o.k, give);
+                } else if (n > o.k) {
+                    order_list(tops, n, tid, o.k, give);
                     n = o.k;
                 } else {
-                    for (int i = tid; i < n; i += TH) give(i, tops[0].list[i]);
+                    for (int i = tid; i < n; i += TH) give(i, tops.list[i]);
                 }
                 if (tid == 0) st_cluster_u32(cluster_map(smem_u32(&lists.count[rank]), 0), n);
-                send_next();
             }
             cluster_sync();
-            if (rank == 0) st = join_cluster<TH, true>(joint[0], tid, cluster, 0, c2);
+            if (rank == 0) st = join_cluster<TH, true>(joint, tid, cluster, 0, c2);
         }
         if (rank == 0) {
             if (tid == 0) put_values(o, r, t, xt, in.c, st);
             if constexpr (kTop) {
-                const bool broken = !(st.s < kInf);
-                const float ln_s = ln(st.s);
-                const int64_t at = r * o.k;
-                auto out = [=](int place, Key key) {
-                    if (o.top_ids != nullptr) o.top_ids[at + place] = key ? key_id(key) : -1;
-                    if (o.top_logprob != nullptr)
-                        o.top_logprob[at + place] =
-                            broken ? NAN : key ? log_prob(key_value(key), in.c, st.m, ln_s) : -kInf;
-                };
                 const bool over = n > TopShared<TH>::kCap;
-                if (lc) {
-                    n = 0;
-                    for (int l = 0; l < cluster; ++l) {
-                        for (int e = tid; e < lists.count[l]; e += TH)
-                            tops[0].list[n + e] = lists.of[l][e];
-                        n += lists.count[l];
-                    }
-                } else if (over && !broken) {
-                    n = take_rounds<TH>(tops[group], p, buf, edge, tid, o.k, out);
-                }
-                if (!lc) send_next();
-                if (broken) n = 0;
-                else if (lc || !over) order_list(tops[group], n, tid, o.k, out);
-                for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
+                if (lc) put_cluster_top(tops, lists, cluster, o, r, st, in.c, tid);
+                else put_top<TH>(tops, o, r, n, over, st, in.c, tid, p, vectors, edge);
             }
         }
-        if (!more) break;
-        if (lc) cluster_sync();  // the first CTA has read what the others gave it
+        if (lc && row.r < in.rows) cluster_sync();  // the first CTA has read what it was given
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!started) cluster_wait();
 }
 
@@ -482,12 +708,11 @@ template <typename T, bool kTop>
 cudaError_t forward_of(int threads, const RowsIn& in, const TokensIn& tk, const ValuesOut& o,
                        cudaStream_t s) {
     constexpr int kShort = kTop ? 32 : 16;
-    constexpr int kLists = kTop ? 18 * 1024 : 1024;  // static shared memory, rounded up
-    switch (threads) {
-        case kShort: return launch_rows<&k_logprob<T, kShort, kTop>, kShort>(in, kTop ? 5 * 1024 : 512, s, in, tk, o);
-        case 128: return launch_rows<&k_logprob<T, 128, kTop>, 128>(in, kLists, s, in, tk, o);
-        default: return launch_rows<&k_logprob<T, 256, kTop>, 256>(in, kLists, s, in, tk, o);
-    }
+    if (threads == kShort)  // the last figures: static shared memory, rounded up
+        return launch_rows<&k_logprob<T, kShort, kTop>, kShort>(in, kTop ? 5 * 1024 : 512, s, in, tk, o);
+    RowsIn with_ring = in;
+    with_ring.slots = kStages * kChunk + (kTop && in.log_cluster ? (int)sizeof(TopLists) / 16 + 1 : 0);
+    return launch_rows<&k_logprob_long<T, kTop>, kLong>(with_ring, kTop ? 14 * 1024 : 1024, s, with_ring, tk, o);
 }
 
 template <typename T>
@@ -524,7 +749,7 @@ extern "C" int mimi_rvq_token_logprob(const void* logits, int dtype, int64_t S, 
     if (top_k > 0 && (!maybe_on_device(top_ids, 4, dev) || !maybe_on_device(top_logprob, 4, dev)))
         return MIMI_RVQ_EINVAL;
     const int k = top_ids != nullptr || top_logprob != nullptr ? top_k : 0;
-    const Shape sh = shape_of(S * n, V, size, k == 0 ? 16 : k <= kWarpTop ? 32 : 0);
+    const Shape sh = shape_of(S * n, V, size, k == 0 ? 16 : k <= kWarpTop ? 32 : 0, false);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
                     slots_of(V, size, sh.log_cluster)};
     const TokensIn tk{tokens, tok_stride_s, tok_stride_n, pad,
@@ -560,7 +785,7 @@ extern "C" int mimi_rvq_token_logprob_grad(
         !maybe_on_device(logprob, 4, dev) || !maybe_on_device(entropy, 4, dev) ||
         !maybe_on_device(lse, 4, dev) || !maybe_on_device(n_bad, 8, dev))
         return MIMI_RVQ_EINVAL;
-    const Shape sh = shape_of(S * n, V, size, 16);
+    const Shape sh = shape_of(S * n, V, size, 16, true);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
                     slots_of(V, size, sh.log_cluster)};
     const TokensIn tk{tokens, tok_stride_s, tok_stride_n, pad,
