@@ -304,6 +304,22 @@ __device__ __forceinline__ void fetch(uint4* buf, const Part<T>& p, int tid) {
 #pragma unroll 4
     for (int i = tid; i < p.nv; i += TH) copy16(buf + i, src + (size_t)i * Elem<T>::kPer);
 }
+// The next row's vectors, sent for as soon as this row's are no longer needed: one by one where
+// the last pass has read a place, the rest when it is done.
+template <typename T>
+struct Next {
+    uint4* buf;
+    const T* src;
+    int nv;
+    __device__ __forceinline__ void refill(int i) const {
+        if (i < nv) copy16(buf + i, src + (size_t)i * Elem<T>::kPer);
+    }
+    // places that this row's nv vectors did not reach
+    template <int TH>
+    __device__ __forceinline__ void rest(int old_nv, int tid) const {
+        for (int i = old_nv + ((tid - old_nv) % TH + TH) % TH; i < nv; i += TH) refill(i);
+    }
+};
 __device__ __forceinline__ void arrived() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void store16(void* p, const uint32_t (&w)[4]) {
@@ -377,10 +393,10 @@ struct Stats {
 };
 
 // A warp's statistics over its threads' vectors and edge values (-inf for none): m is the warp's,
-// s and w the thread's own. top: the thread's own maximum.
-template <int TH, bool kW, typename T>
+// s and w the thread's own. top: the thread's own maximum. after(i): vector i has been read.
+template <int TH, bool kW, typename T, typename After>
 __device__ __forceinline__ Stats pass(const uint4* buf, int nv, int tid, float edge, float c2,
-                                      float& top) {
+                                      float& top, After&& after) {
     if constexpr (sizeof(T) == 4) {
         top = edge;
         each_vector<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
@@ -405,16 +421,18 @@ __device__ __forceinline__ Stats pass(const uint4* buf, int nv, int tid, float e
         }
     };
     if (!k.far)
-        each_vector<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
+        each_vector<TH>(buf, nv, tid, [&](int i, const uint32_t (&w)[4]) {
             Pair t[Elem<T>::kPer / 2];
             exponents<T, kW, false>(w, k, t);
             add(t);
+            after(i);
         });
     else
-        each_in_turn<TH>(buf, nv, tid, [&](int, const uint32_t (&w)[4]) {
+        each_in_turn<TH>(buf, nv, tid, [&](int i, const uint32_t (&w)[4]) {
             Pair t[Elem<T>::kPer / 2];
             exponents<T, kW, true>(w, k, t);
             add(t);
+            after(i);
         });
     float s, s1, w = 0.f, w1 = 0.f;
     halves(s2, s, s1);
@@ -474,6 +492,7 @@ struct Joint {
 // may leave what the others need after it in shared memory).
 template <int TH, bool kW>
 __device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, int parity, float c2) {
+    // threads past TH only read
     st.s = lanes_sum<TH>(st.s);
     if constexpr (kW) st.w = lanes_sum<TH>(st.w);
     if constexpr (TH <= 32) {
@@ -482,7 +501,7 @@ __device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, int
     } else {
         const int lane = tid & 31;
         float(&at)[3][(TH + 31) / 32] = j.warp[parity];
-        if (lane == 0) {
+        if (lane == 0 && tid < TH) {
             at[0][tid / 32] = st.m;
             at[1][tid / 32] = st.s;
             if constexpr (kW) at[2][tid / 32] = st.w;
@@ -531,7 +550,7 @@ template <int TH>
 __host__ __device__ constexpr int block_of() { return TH > 128 ? TH : 128; }
 // CTAs per SM a kernel is compiled for: 64 registers a thread
 template <int TH>
-__host__ __device__ constexpr int blocks_of() { return 1024 / block_of<TH>(); }
+__host__ __device__ constexpr int blocks_of() { return TH == 384 ? 3 : 1024 / block_of<TH>(); }
 // A thread's number in its group, and its group's in the CTA.
 template <int TH>
 __device__ __forceinline__ int thread_in_group() { return TH < block_of<TH>() ? threadIdx.x % TH : threadIdx.x; }
@@ -610,9 +629,10 @@ inline bool apart_or_same(const void* x, int64_t ss, int64_t sn, const void* d, 
 
 // One launch over all rows: as many groups as are resident, each with `slots` places of 16 bytes
 // in dynamic shared memory, or one for each row if they are fewer.
-template <auto kernel, int TH, typename... Args>
+// kMore: threads of a CTA beside the row's TH.
+template <auto kernel, int TH, int kMore, typename... Args>
 cudaError_t launch_rows(const RowsIn& in, int static_smem, cudaStream_t stream, Args... args) {
-    constexpr int block = block_of<TH>(), rows_per = block / TH;
+    constexpr int block = block_of<TH>() + kMore, rows_per = block_of<TH>() / TH;
     const int smem = rows_per * in.slots * 16;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;

@@ -2,11 +2,11 @@
 // Declared in include/mimi_rvq_streams.h; layout and statistics in logits.cuh.
 //
 // The row's listed tokens are taken out of the pass: once the row is in shared
-// memory the group's first warp reads the listed logits there and puts -inf in
-// their places (an id listed twice is seen by the entries' numbers that are
-// written there in between). The pass then gives the statistics of the rest,
-// from which both the whole row's (joined with the listed logits) and the tail
-// class's probability follow without cancellation, however certain
+// memory its lister (a warp beside the row's threads; half a warp's row lists for
+// itself) reads the listed logits there and puts -inf in their places. The pass
+// then gives the statistics of the rest, from which both the whole row's (joined
+// with the listed logits) and the tail class's probability follow without
+// cancellation, however certain
 // the student is of the list. With (m_r, s_r) the rest's and ln s the row's:
 //     ln p_i = c (x_i - m) - ln s,   ln p_rest = c (m_r - m) + ln s_r - ln s,
 //     d x_i = g c (Q p_i - q_r e^{c (x_i - m_r)} / s_r)       unlisted
@@ -35,8 +35,7 @@ struct TeacherIn {
     unsigned long long* n_bad;
 };
 
-// A place of the list: kept by the group's first lanes (16 or 32), lane l having places l,
-// l + lanes, ...
+// A place of the list: the lister's lane l has places l, l + lanes, ...
 struct alignas(16) Entry {
     int id;          // -1: an empty place
     float q, lq, x;  // weight, its logarithm, the student's logit
@@ -60,28 +59,40 @@ struct ListJoint {
 template <typename T>
 using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
 
+constexpr int kShortTop = 32;  // longest list of half a warp's row
+
+// Threads beside a CTA's row: its lister.
+template <int TH>
+__host__ __device__ constexpr int lister_of() { return TH > 32 ? 32 : 0; }
+template <int TH>
+__host__ __device__ constexpr int distill_blocks() { return 1024 / (block_of<TH>() + lister_of<TH>()); }
+
 template <typename T, int TH, bool kGrad>
-__global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(RowsIn in, TeacherIn te) {
+__global__ void __launch_bounds__(block_of<TH>() + lister_of<TH>(), distill_blocks<TH>())
+    k_distill(RowsIn in, TeacherIn te) {
     constexpr int kRows = block_of<TH>() / TH, kPer = Part<T>::kPer;
+    constexpr int L = lanes_of<TH>(), kLane = (TH <= 32 ? kShortTop : kMaxTop) / L;
+    using B = Bits<T>;
     extern __shared__ uint4 buffers[];  // [groups][slots]: the row's vectors, then the list
     __shared__ Joint<TH> joint[kRows];
     __shared__ ListShared<T> lists[kRows];
     __shared__ ListJoint listed_of;
-    const int tid = thread_in_group<TH>();
-    const int group = group_in_block<TH>();
+    const int tid = TH > 32 ? threadIdx.x : thread_in_group<TH>();
+    const int group = TH > 32 ? 0 : group_in_block<TH>();
     const int lc = TH <= 32 ? 0 : in.log_cluster, cluster = 1 << lc;
     const int rank = lc ? (int)cluster_ctarank() : 0;
-    const bool first_lanes = rank == 0 && tid < lanes_of<TH>();  // have the row's edges
+    const bool worker = tid < TH, first_lanes = rank == 0 && tid < L;  // the latter have the edges
+    const bool lister = TH <= 32 || !worker;
+    const int me = TH <= 32 ? tid : tid - TH;  // the lister's lane
+    const unsigned mask = lane_mask<TH>();
     uint4* buf = buffers + (size_t)group * in.slots;
     Entry* list = reinterpret_cast<Entry*>(buf + in.slots - te.k);
     const float c2 = in.c * kLog2e;
     ListShared<T>& ls = lists[group];
-    constexpr int L = lanes_of<TH>(), kLane = kMaxTop / L;
-    const unsigned mask = lane_mask<TH>();
-    const bool lister = tid < L;
     if (lc) cluster_sync();  // every CTA runs before one writes to another
     RowWalk row((int64_t)(blockIdx.x >> lc) * kRows + group,
                 (int64_t)(gridDim.x >> lc) * kRows, in.n);
+    if (row.r >= in.rows) return;
     // the row's weight and list: loaded a row ahead
     float g_next = 1.f;
     int id_next[kLane];
@@ -94,7 +105,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
 #pragma unroll
             for (int i = 0; i < kLane; ++i) {
                 if (i * L >= te.k) break;
-                const int e = tid + L * i;
+                const int e = me + L * i;
                 id_next[i] = -1;
                 if (e < te.k) {
                     id_next[i] = __ldg(te.ids + at + e);
@@ -104,105 +115,131 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
             }
         }
     };
+    // a row's part of what is read for it: its share of the vectors, and an element beside them
+    struct At {
+        Part<T> p;
+        int64_t r, s;
+        int j, ie;
+        float g, edge;
+        bool skip;  // a gradient of weight 0 alone: zeros, whatever the row is
+    };
+    auto at_row = [&]() {
+        At at{Part<T>(static_cast<const T*>(in.x) + row.s * in.ss + row.j * in.sn, in.V, rank, lc),
+              row.r, row.s, row.j, -1, kGrad ? g_next : 1.f, -kInf, false};
+        at.skip = kGrad && at.g == 0.f && te.loss == nullptr;
+        at.ie = first_lanes ? at.p.edge(tid) : -1;
+        if (!at.skip && at.ie >= 0) at.edge = widen(at.p.x[at.ie]);
+        return at;
+    };
     list_at();
-    for (int parity = 0; row.r < in.rows;) {
-        const int64_t r = row.r;
-        const Part<T> p(static_cast<const T*>(in.x) + row.s * in.ss + row.j * in.sn, in.V, rank, lc);
-        T* d = static_cast<T*>(te.d) + row.s * te.d_ss + row.j * te.d_sn;
+    At now = at_row();
+    if (!now.skip && worker) fetch<TH>(buf, now.p, tid);
+    for (int parity = 0;;) {
+        const Part<T> p = now.p;
+        const int64_t r = now.r;
+        const int ie = now.ie;
+        const float g = now.g;
+        float edge = now.edge;
+        const bool skip = now.skip;
+        T* d = static_cast<T*>(te.d) + now.s * te.d_ss + now.j * te.d_sn;
         const bool wide = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(p.x)) & 15u) == 0;
         T* out = d + p.first;
-        const float g = kGrad ? g_next : 1.f;
-        const bool skip = kGrad && g == 0.f && te.loss == nullptr;  // zeros, whatever the row is
-        const int ie = first_lanes ? p.edge(tid) : -1;
-        float edge = -kInf;
-        if (!skip) {
-            fetch<TH>(buf, p, tid);
-            if (ie >= 0) edge = widen(p.x[ie]);
-        }
         int n = 0, bad = 0;
         float tmax = -kInf;
         bool broken = false;  // NaN or +inf among the entries
+        unsigned first = 0;   // bit i: entry me + L i is this share's, the first of its id
+        bool twice = false;   // some id is listed twice
         if (lister) {
+            __syncwarp(mask);  // the last row's list has been read
 #pragma unroll
             for (int i = 0; i < kLane; ++i) {
                 if (i * L >= te.k) break;
-                const int e = tid + L * i;
-                if (e >= te.k) continue;
-                int id = id_next[i];
-                if (id >= in.V) ++bad;
-                if (id < 0 || id >= in.V) id = -1;
-                const float t = id >= 0 ? t_next[i] : -kInf;
-                n += id >= 0;
-                tmax = fmaxf(tmax, t);
-                broken |= !(t < kInf);
-                list[e].id = id;
-                list[e].lq = t;
+                const int e = me + L * i;
+                int id = -1 - e;  // empty places differ
+                if (e < te.k) {
+                    const int given = id_next[i];
+                    bad += given >= in.V;
+                    if (given >= 0 && given < in.V) id = given;
+                    const float t = id >= 0 ? t_next[i] : -kInf;
+                    n += id >= 0;
+                    tmax = fmaxf(tmax, t);
+                    broken |= !(t < kInf);
+                    list[e].id = id < 0 ? -1 : id;
+                    list[e].lq = t;
+                }
+                const unsigned same = __match_any_sync(mask, id);
+                bool again = id >= 0 && (same & ((1u << (threadIdx.x & 31)) - 1u));
+                __syncwarp(mask);
+                for (int l = 0; l < i * L; ++l) again |= id >= 0 && list[l].id == id;
+                twice |= again;
+                if (id >= 0 && !again && (p.place(id) >= 0 || (rank == 0 && p.in_edges(id))))
+                    first |= 1u << i;
             }
+            twice = __any_sync(mask, twice);
             if (bad && rank == 0 && te.n_bad != nullptr)
                 atomicAdd(te.n_bad, (unsigned long long)bad);
+            tmax = lanes_max<TH>(tmax);
+            broken = __any_sync(mask, broken);
+            n = __any_sync(mask, n > 0);
         }
         row.next(in.n);
+        const bool more = row.r < in.rows;
         list_at();
         bool empty = true;
-        unsigned first = 0;  // bit i: entry tid + L i is this share's, the first of its id
-        bool twice = false;  // some id is listed twice
         if (!skip) {
             arrived();
             if (first_lanes && tid < 16 && ie >= 0) narrow(edge, &ls.edge[tid]);
             group_sync<TH>();  // the row is here
             if (lister) {
-                using B = Bits<T>;
-                // where a listed element of this share is
-                auto cell = [&](int id) {
-                    const int q = p.place(id);
-                    return q >= 0 ? reinterpret_cast<B*>(buf) + q
-                                  : reinterpret_cast<B*>(ls.edge) + p.edge_lane(id);
-                };
-                for (int e = tid, i = 0; e < te.k; e += L, ++i) {
-                    const int id = list[e].id;
-                    if (id < 0) continue;
-                    if (p.place(id) >= 0 || (rank == 0 && p.in_edges(id))) {
-                        first |= 1u << i;
-                        list[e].x = widen(*reinterpret_cast<const T*>(cell(id)));
-                    } else if (rank == 0) {
-                        list[e].x = widen(p.x[id]);  // another CTA's; for the loss
+                // the listed elements of this share: read, then hidden
+                auto each = [&](auto&& f) {
+                    for (int e = me, i = 0; e < te.k; e += L, ++i) {
+                        const int id = list[e].id, q = p.place(id);
+                        if (id < 0 || (q < 0 && (rank != 0 || !p.in_edges(id)))) continue;
+                        f(e, q >= 0 ? reinterpret_cast<B*>(buf) + q
+                                    : reinterpret_cast<B*>(ls.edge) + p.edge_lane(id));
                     }
-                }
-                __syncwarp(mask);
-                auto each_first = [&](auto&& f) {
-                    for (int e = tid, i = 0; e < te.k; e += L, ++i)
-                        if ((first >> i) & 1u) f(e, i);
-                    __syncwarp(mask);
                 };
-                each_first([&](int e, int) { *cell(list[e].id) = (B)e; });
-                each_first([&](int e, int) { twice |= *cell(list[e].id) != (B)e; });
-                each_first([&](int e, int) { *cell(list[e].id) = (B)Elem<T>::kFill; });
-                twice = __any_sync(mask, twice);
-                if (twice)  // the first of equal ids stands for all
-                    each_first([&](int e, int i) {
-                        for (int l = 0; l < e; ++l)
-                            if (list[l].id == list[e].id) first &= ~(1u << i);
+                auto read = [&](int e, B* at) { list[e].x = widen(*reinterpret_cast<const T*>(at)); };
+                auto hide = [&](int, B* at) { *at = (B)Elem<T>::kFill; };
+                if (!twice) {
+                    each([&](int e, B* at) {
+                        read(e, at);
+                        hide(e, at);
                     });
-                const bool some = __any_sync(mask, n > 0);
-                tmax = lanes_max<TH>(tmax);
-                broken = __any_sync(mask, broken);
-                if (tid == 0) ls.empty = !some || (!te.tail && tmax == -kInf && !broken);
-                if (ie >= 0) edge = widen(ls.edge[tid]);
+                } else {
+                    each(read);
+                    __syncwarp(mask);
+                    each(hide);
+                }
+                if (lc && rank == 0)  // other CTAs' elements; for the loss
+                    for (int e = me; e < te.k; e += L) {
+                        const int id = list[e].id;
+                        if (id >= 0 && p.place(id) < 0 && !p.in_edges(id)) list[e].x = widen(p.x[id]);
+                    }
+                if (me == 0) ls.empty = !n || (!te.tail && tmax == -kInf && !broken);
             }
             group_sync<TH>();  // the listed tokens are hidden
+            if (ie >= 0) edge = widen(ls.edge[tid]);
             empty = ls.empty != 0;
         }
+        if (more) now = at_row();
+        const Next<T> next{buf, now.p.x + now.p.first, more && !now.skip ? now.p.nv : 0};
         Stats rest{-kInf, 0.f, 0.f}, all{-kInf, 0.f, 0.f};
         if (!empty) {
-            float top;
-            rest = pass<TH, false, T>(buf, p.nv, tid, edge, c2, top);
+            if (worker) {
+                float top;
+                rest = pass<TH, false, T>(buf, p.nv, tid, edge, c2, top, [&](int i) {
+                    if (!kGrad) next.refill(i);
+                });
+            }
             if (lister) {  // the weights and this share's listed logits
                 float Q = 1.f, tail_q = 0.f;
                 if (te.tail) {
                     // the tail's weight is what the list leaves of 1: in float64, or a tail of
                     // 1e-6 would be rounding
                     double sum = 0.0;
-                    for (int e = tid; e < te.k; e += L) {
+                    for (int e = me; e < te.k; e += L) {
                         const bool in_list = list[e].id >= 0;
                         list[e].q = in_list ? expf(list[e].lq) : 0.f;
                         if (in_list) sum += exp((double)list[e].lq);
@@ -213,32 +250,32 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
                 } else {
                     const float tm = tmax == -kInf ? 0.f : tmax;
                     float sum = 0.f;
-                    for (int e = tid; e < te.k; e += L)
+                    for (int e = me; e < te.k; e += L)
                         if (list[e].id >= 0) sum += expf(list[e].lq - tm);
                     sum = lanes_sum<TH>(sum);
                     if (broken) Q = NAN;
                     const float ln_sum = logf(sum);
-                    for (int e = tid; e < te.k; e += L) {
+                    for (int e = me; e < te.k; e += L) {
                         const float lq = (list[e].lq - tm) - ln_sum;
                         list[e].lq = lq;
                         list[e].q = list[e].id >= 0 ? expf(lq) : 0.f;
                     }
                 }
                 float m = -kInf, sum = 0.f;
-                for (int e = tid, i = 0; e < te.k; e += L, ++i)
+                for (int e = me, i = 0; e < te.k; e += L, ++i)
                     if ((first >> i) & 1u) m = fmaxf(m, list[e].x);
                 m = lanes_max<TH>(m);
-                for (int e = tid, i = 0; e < te.k; e += L, ++i)
+                for (int e = me, i = 0; e < te.k; e += L, ++i)
                     if ((first >> i) & 1u) sum += ex2(exponent(list[e].x, m, c2));
                 sum = lanes_sum<TH>(sum);
-                if (tid == 0) {
+                if (me == 0) {
                     ls.m = m;
                     ls.s = sum;
                     ls.Q = Q;
                     ls.tail_q = tail_q;
                 }
-                if (lc && tid < cluster) {
-                    const uint32_t to = cluster_map(smem_u32(&listed_of.cta[parity][0][rank]), tid);
+                if (lc && me < cluster) {
+                    const uint32_t to = cluster_map(smem_u32(&listed_of.cta[parity][0][rank]), me);
                     st_cluster_f32(to, m);
                     st_cluster_f32(to + 4 * kMaxCluster, sum);
                 }
@@ -265,20 +302,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
             qr = rest.s == 0.f ? 0.f : ls.tail_q;
             Q = te.tail ? ls.Q + qr : ls.Q;
         }
-        if (te.loss != nullptr && first_lanes) {
-            const float ln_s = ln(all.s);
-            float part = 0.f;
-            if (!empty) {
-                for (int e = tid; e < te.k; e += L)
-                    if (list[e].id >= 0 && list[e].q != 0.f)
-                        part += list[e].q * (list[e].lq - (all.s == 0.f ? -kInf : log_prob(list[e].x, in.c, all.m, ln_s)));
-                part = lanes_sum<TH>(part);
-                if (qr > 0.f)
-                    part += qr * (logf(qr) - (in.c * (rest.m - all.m) + ln(rest.s) - ln_s));
-            }
-            if (tid == 0) te.loss[r] = Q != Q ? NAN : part;
-        }
-        if constexpr (kGrad) {
+        if (kGrad && worker) {
             if (none) {
                 for (int i = tid; i < p.nv; i += TH) {
                     const float y[kPer] = {};
@@ -313,32 +337,50 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>()) k_distill(Row
                         put(i, t, wide);
                     });
                 if (ie >= 0) narrow(ex2(exponent(edge, rest.m, c2)) * f0, d + ie);
-                group_sync<TH>();  // the listed tokens' places hold the rest's gradient by now
-                if (lister)
-                    for (int e = tid, i = 0; e < te.k; e += L, ++i)
-                        if ((first >> i) & 1u) {
-                            const int id = list[e].id;
-                            float w = list[e].q;
-                            if (twice) {
-                                w = 0.f;
-                                for (int l = 0; l < te.k; ++l)
-                                    if (list[l].id == id) w += list[l].q;
-                            }
-                            const float pi = ex2(exponent(list[e].x, all.m, c2)) * inv;
-                            narrow(gc * (Q * pi - w), d + id);
-                        }
             }
         }
-        group_sync<TH>();  // the list and the row's place are free again
+        if (more && worker) next.template rest<TH>(kGrad || empty ? 0 : p.nv, tid);
+        if (te.loss != nullptr && lister && rank == 0) {
+            const float ln_s = ln(all.s);
+            float part = 0.f;
+            if (!empty) {
+                for (int e = me; e < te.k; e += L)
+                    if (list[e].id >= 0 && list[e].q != 0.f)
+                        part += list[e].q * (list[e].lq - (all.s == 0.f ? -kInf : log_prob(list[e].x, in.c, all.m, ln_s)));
+                part = lanes_sum<TH>(part);
+                if (qr > 0.f)
+                    part += qr * (logf(qr) - (in.c * (rest.m - all.m) + ln(rest.s) - ln_s));
+            }
+            if (me == 0) te.loss[r] = Q != Q ? NAN : part;
+        }
+        if (kGrad && !none) {
+            group_sync<TH>();  // the listed tokens' places hold the rest's gradient by now
+            if (lister) {
+                const float gc = g * in.c, inv = reciprocal(all.s);
+                for (int e = me, i = 0; e < te.k; e += L, ++i)
+                    if ((first >> i) & 1u) {
+                        const int id = list[e].id;
+                        float w = list[e].q;
+                        if (twice) {
+                            w = 0.f;
+                            for (int l = 0; l < te.k; ++l)
+                                if (list[l].id == id) w += list[l].q;
+                        }
+                        const float pi = ex2(exponent(list[e].x, all.m, c2)) * inv;
+                        narrow(gc * (Q * pi - w), d + id);
+                    }
+            }
+        }
+        if (!more) break;
     }
 }
 
 template <typename T, bool kGrad>
 cudaError_t distill_of(int threads, const RowsIn& in, const TeacherIn& te, cudaStream_t s) {
     switch (threads) {
-        case 16: return launch_rows<&k_distill<T, 16, kGrad>, 16>(in, 1024, s, in, te);
-        case 128: return launch_rows<&k_distill<T, 128, kGrad>, 128>(in, 1024, s, in, te);
-        default: return launch_rows<&k_distill<T, 256, kGrad>, 256>(in, 1024, s, in, te);
+        case 16: return launch_rows<&k_distill<T, 16, kGrad>, 16, lister_of<16>()>(in, 1024, s, in, te);
+        case 128: return launch_rows<&k_distill<T, 128, kGrad>, 128, lister_of<128>()>(in, 1024, s, in, te);
+        default: return launch_rows<&k_distill<T, 256, kGrad>, 256, lister_of<256>()>(in, 1024, s, in, te);
     }
 }
 
@@ -366,7 +408,7 @@ int distill(const void* logits, int dtype, int64_t S, int n, int V, int64_t stri
                  !apart_or_same(logits, stride_s, stride_n, dlogits, d_stride_s, d_stride_n, S, n,
                                 V, size)))
         return MIMI_RVQ_EINVAL;
-    const Shape sh = shape_of(S * n, V, size, 16, true);
+    const Shape sh = shape_of(S * n, V, size, k <= kShortTop ? 16 : 0, true);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
                     slots_of(V, size, sh.log_cluster) + k};
     const TeacherIn te{ids, teacher, teacher_dtype == MIMI_RVQ_BF16, k, tail, g, loss, dlogits,

@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
         const float xt = t >= 0 ? widen(p.x[t]) : 0.f;
         arrived();
         float top;
-        Stats st = pass<TH, true, T>(buf, p.nv, tid, edge, c2, top);
+        Stats st = pass<TH, true, T>(buf, p.nv, tid, edge, c2, top, [](int) {});
         row.next(in.n);
         const bool more = row.r < in.rows;
         auto send_next = [&]() {
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
         if (!zero || values) {
             arrived();
             float top;
-            st = pass<TH, true, T>(buf, p.nv, tid, edge, c2, top);
+            st = pass<TH, true, T>(buf, p.nv, tid, edge, c2, top, [](int) {});
             st = join_row<TH, true>(joint[group], st, tid, cluster, rank, parity, c2);
             parity ^= 1;
             if (first_warp && tid == 0) put_values(o, r, t, xt, in.c, st);
@@ -709,19 +709,19 @@ cudaError_t forward_of(int threads, const RowsIn& in, const TokensIn& tk, const 
                        cudaStream_t s) {
     constexpr int kShort = kTop ? 32 : 16;
     if (threads == kShort)  // the last figures: static shared memory, rounded up
-        return launch_rows<&k_logprob<T, kShort, kTop>, kShort>(in, kTop ? 5 * 1024 : 512, s, in, tk, o);
+        return launch_rows<&k_logprob<T, kShort, kTop>, kShort, 0>(in, kTop ? 5 * 1024 : 512, s, in, tk, o);
     RowsIn with_ring = in;
     with_ring.slots = kStages * kChunk + (kTop && in.log_cluster ? (int)sizeof(TopLists) / 16 + 1 : 0);
-    return launch_rows<&k_logprob_long<T, kTop>, kLong>(with_ring, kTop ? 14 * 1024 : 1024, s, with_ring, tk, o);
+    return launch_rows<&k_logprob_long<T, kTop>, kLong, 0>(with_ring, kTop ? 14 * 1024 : 1024, s, with_ring, tk, o);
 }
 
 template <typename T>
 cudaError_t gradient_of(int threads, const RowsIn& in, const TokensIn& tk, const GradIn& g,
                         const ValuesOut& o, cudaStream_t s) {
     switch (threads) {
-        case 16: return launch_rows<&k_logprob_grad<T, 16>, 16>(in, 1024, s, in, tk, g, o);
-        case 128: return launch_rows<&k_logprob_grad<T, 128>, 128>(in, 1024, s, in, tk, g, o);
-        default: return launch_rows<&k_logprob_grad<T, 256>, 256>(in, 1024, s, in, tk, g, o);
+        case 16: return launch_rows<&k_logprob_grad<T, 16>, 16, 0>(in, 1024, s, in, tk, g, o);
+        case 128: return launch_rows<&k_logprob_grad<T, 128>, 128, 0>(in, 1024, s, in, tk, g, o);
+        default: return launch_rows<&k_logprob_grad<T, 256>, 256, 0>(in, 1024, s, in, tk, g, o);
     }
 }
 
