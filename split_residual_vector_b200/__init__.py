@@ -379,27 +379,35 @@ def _call_on(device, stream, call):
     made current first where they are not, so that outputs are allocated there too."""
     import torch
     if stream is not None:
-        with torch.cuda.stream(stream):
-            if stream.device == device:
-                return call(stream.cuda_stream)
-            with torch.cuda.device(device):
-                return call(stream.cuda_stream)
+        with torch.cuda.stream(stream), torch.cuda.device(device):
+            return call(stream.cuda_stream)
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return call(torch.cuda.current_stream().cuda_stream)
     return call(torch._C._cuda_getCurrentRawStream(device.index))
 
 
-def _values_for(logits, lead, tokens, top_k):
-    """Outputs of token_logprobs: one allocation for the values, one for the lists."""
+def _new_values(lead, device, tokens, top_k):
+    """Outputs of token_logprobs and their pointers."""
     import torch
-    f32 = torch.float32
-    v = logits.new_empty((3, *lead), dtype=f32).unbind(0)
-    if not top_k:
-        return TokenLogprobs(None if tokens is None else v[0], v[1], v[2], None, None)
-    top = logits.new_empty((2, *lead, top_k), dtype=f32).unbind(0)
-    return TokenLogprobs(None if tokens is None else v[0], v[1], v[2], top[0].view(torch.int32),
-                         top[1])
+    entropy = torch.empty(*lead, dtype=torch.float32, device=device)
+    lse = torch.empty_like(entropy)
+    logprob = None if tokens is None else torch.empty_like(entropy)
+    ids = top = None
+    if top_k:
+        top = torch.empty(*lead, top_k, dtype=torch.float32, device=device)
+        ids = torch.empty_like(top, dtype=torch.int32)
+    v = TokenLogprobs(logprob, entropy, lse, ids, top)
+    return v, [None if t is None else t.data_ptr() for t in v]
+
+
+def _given_values(v, lead, device, top_k):
+    """The same of outputs that the caller gave."""
+    import torch
+    f32, top = torch.float32, (*lead, top_k)
+    return v, [_row_array(v.logprob, lead, f32, device), _row_array(v.entropy, lead, f32, device),
+               _row_array(v.lse, lead, f32, device), _row_array(v.top_ids, top, torch.int32, device),
+               _row_array(v.top_logprob, top, f32, device)]
 
 
 def _logit_rows(logits):
@@ -440,8 +448,9 @@ def _bad_counter(n_bad, device):
 
 def _gradient(out, logits):
     """The gradient's tensor and its (stride_s, stride_n)."""
+    import torch
     if out is None:
-        out = logits.new_empty(logits.shape)
+        out = torch.empty(*logits.shape, dtype=logits.dtype, device=logits.device)
     assert out.shape == logits.shape and out.dtype == logits.dtype and out.device == logits.device
     st = out.stride()
     assert out.shape[-1] <= 1 or st[-1] == 1
@@ -457,21 +466,17 @@ def token_logprobs(logits, tokens=None, pad=-1, scale=1.0, top_k=0, out=None, n_
     top_k = 0. scale is 1 / temperature. out: TokenLogprobs of tensors to write, None in the
     place of values that are not wanted. n_bad: optional CUDA int64 [1] (caller-zeroed)
     counting tokens past V."""
-    import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
-    dev, f32, top_k = logits.device, torch.float32, int(top_k)
+    dev, top_k = logits.device, int(top_k)
     tok = _row_tokens(tokens, lead, dev)
 
     def call(raw):
-        r = _values_for(logits, lead, tokens, max(top_k, 0)) if out is None else out
-        top = (*lead, top_k)
+        v, pointers = (_new_values(lead, dev, tokens, max(top_k, 0)) if out is None
+                       else _given_values(out, lead, dev, top_k))
         _check(library().mimi_rvq_token_logprob(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *tok, pad, scale, top_k,
-            _row_array(r.logprob, lead, f32, dev), _row_array(r.entropy, lead, f32, dev),
-            _row_array(r.lse, lead, f32, dev), _row_array(r.top_ids, top, torch.int32, dev),
-            _row_array(r.top_logprob, top, f32, dev), _bad_counter(n_bad, dev), raw),
-            "mimi_rvq_token_logprob")
-        return r
+            logits.data_ptr(), dt, S, n, V, ss, sn, *tok, pad, scale, top_k, *pointers,
+            _bad_counter(n_bad, dev), raw), "mimi_rvq_token_logprob")
+        return v
 
     return _call_on(dev, stream, call)
 
@@ -490,15 +495,14 @@ def token_logprobs_grad(logits, tokens=None, g_logprob=None, g_entropy=None, g_l
 
     def call(raw):
         d, d_strides = _gradient(out, logits)
-        v = _values_for(logits, lead, tokens, 0) if values is True else (values or _NO_VALUES)
+        v, pointers = (_new_values(lead, dev, tokens, 0) if values is True
+                       else _given_values(values or _NO_VALUES, lead, dev, 0))
         assert v.top_ids is None and v.top_logprob is None, "the gradient call lists no tokens"
         _check(library().mimi_rvq_token_logprob_grad(
             logits.data_ptr(), dt, S, n, V, ss, sn, *tok, pad, scale,
             _row_array(g_logprob, lead, f32, dev), _row_array(g_entropy, lead, f32, dev),
-            _row_array(g_lse, lead, f32, dev), d.data_ptr(), *d_strides,
-            _row_array(v.logprob, lead, f32, dev), _row_array(v.entropy, lead, f32, dev),
-            _row_array(v.lse, lead, f32, dev), _bad_counter(n_bad, dev), raw),
-            "mimi_rvq_token_logprob_grad")
+            _row_array(g_lse, lead, f32, dev), d.data_ptr(), *d_strides, *pointers[:3],
+            _bad_counter(n_bad, dev), raw), "mimi_rvq_token_logprob_grad")
         return (d, v) if values else d
 
     return _call_on(dev, stream, call)
@@ -525,7 +529,7 @@ def distill_topk(logits, ids, teacher, tail=False, scale=1.0, out=None, n_bad=No
     lists = _teacher_list(ids, teacher, lead, dev)
 
     def call(raw):
-        loss = logits.new_empty(lead, dtype=f32) if out is None else out
+        loss = torch.empty(*lead, dtype=f32, device=dev) if out is None else out
         _check(library().mimi_rvq_distill_topk(
             logits.data_ptr(), dt, S, n, V, ss, sn, *lists, 1 if tail else 0, scale,
             _row_array(loss, lead, f32, dev), _bad_counter(n_bad, dev), raw),
@@ -548,7 +552,7 @@ def distill_topk_grad(logits, ids, teacher, g=None, tail=False, scale=1.0, loss=
 
     def call(raw):
         d, d_strides = _gradient(out, logits)
-        losses = logits.new_empty(lead, dtype=f32) if loss is True else loss
+        losses = torch.empty(*lead, dtype=f32, device=dev) if loss is True else loss
         _check(library().mimi_rvq_distill_topk_grad(
             logits.data_ptr(), dt, S, n, V, ss, sn, *lists, 1 if tail else 0, scale,
             _row_array(g, lead, f32, dev), d.data_ptr(), *d_strides,
