@@ -102,12 +102,12 @@ constexpr int kWarpTop = 24;
 
 template <int TH>
 struct TopShared {
-    static constexpr int kCap = TH == 32 ? 128 : 512;
-    uint32_t most[TH == 32 ? 1 : TH];  // the threads' maxima
+    static constexpr int kCap = TH == 32 ? 128 : 256;
+    alignas(16) uint32_t most[TH == 32 ? 4 : TH];  // the threads' maxima
     float bound;
     int count;
     alignas(16) Key list[kCap + 8];
-    Key last[TH / 32];
+    Key last[TH == 32 ? kCap / 4 : TH / 32];  // a warp: the vectors that have a listed logit
 };
 // The keys that a cluster's CTAs give its first one.
 struct TopLists {
@@ -130,24 +130,21 @@ __device__ __forceinline__ void each_logit(const uint4* buf, const Part<T>& p, i
     if (edge > -kInf) f(edge, p.edge(tid));
 }
 
-// Leaves in sh.bound the largest bound (in steps of 2^16 of the values' order) that k of the
-// threads' maxima reach, or the lowest finite value; called by the first warp behind a barrier.
-template <int TH>
-__device__ __forceinline__ void find_bound(TopShared<TH>& sh, float top, int tid, int k) {
-    constexpr int kN = TH / 32;
-    uint32_t q[kN];
-    uint32_t hi = 0, lo = 0xFFFFFFFFu;
+// The largest bound (in steps of 2^16 of the values' order) that k of a warp's values reach, each
+// lane having kN of them; the lowest finite value where fewer are above it.
+template <int kN>
+__device__ __forceinline__ float bound_of(const uint32_t (&q)[kN], int k) {
+    uint32_t hi = q[0], lo = q[0];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        q[i] = TH == 32 ? order_of(top) : sh.most[tid + 32 * i];
+    for (int i = 1; i < kN; ++i) {
         hi = max(hi, q[i]);
         lo = min(lo, q[i]);
     }
     hi = __reduce_max_sync(kFull, hi);
     lo = __reduce_min_sync(kFull, lo);
-    // bits that all maxima share are the bound's, and k maxima exactly is as good as it gets
+    // bits that all values share are the bound's, and k values exactly is as good as it gets
     uint32_t b = 0;
-    if (k <= TH) {
+    if (k <= 32 * kN) {
         const int top_bit = 31 - __clz(lo ^ hi);  // -1: all are equal
         b = lo == hi ? lo : lo & ~((2u << top_bit) - 1u);
         for (int bit = top_bit; bit >= 16; --bit) {
@@ -159,44 +156,74 @@ __device__ __forceinline__ void find_bound(TopShared<TH>& sh, float top, int tid
             if (n == k) break;
         }
     }
+    return order_value(max(b, kOrderNegInf + 1));
+}
+
+// Leaves a CTA's bound for its k largest logits in sh.bound; called by its first warp when the
+// threads' maxima are there. Lists of up to 24 take the maxima of 4 threads as one value.
+template <int TH>
+__device__ __forceinline__ void find_bound(TopShared<TH>& sh, int tid, int k) {
+    static_assert(TH == 128, "four maxima a lane");
+    const uint4 v = *reinterpret_cast<const uint4*>(&sh.most[4 * tid]);
+    float bound;
+    if (k <= kWarpTop) {
+        const uint32_t q[1] = {max(max(v.x, v.y), max(v.z, v.w))};
+        bound = bound_of(q, k);
+    } else {
+        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+        bound = bound_of(q, k);
+    }
     if (tid == 0) {
-        sh.bound = order_value(max(b, kOrderNegInf + 1));
+        sh.bound = bound;
         sh.count = 0;
     }
 }
 
 // A warp's row: the logits that reach the bound, as unordered keys in sh.list; returns their
-// number, at least min(k, the logits above -inf); past kCap the list is not complete.
+// number, at least min(k, the logits above -inf); past kCap the list is not complete. Vectors
+// with such a logit are listed first, then their elements are spread over the lanes.
 template <typename T>
 __device__ __forceinline__ int collect(TopShared<32>& sh, const Part<T>& p, const uint4* buf,
-                                       float edge, float top, int tid, int k) {
-    constexpr int TH = 32, kCap = TopShared<32>::kCap;
-    find_bound(sh, top, tid, k);
-    group_sync<TH>();
-    const float bound = sh.bound;
-    const int lane = tid & 31;
-    if (__any_sync(kFull, top >= bound)) {  // count each lane's, then give them places
-        int mine = 0;
-        if (top >= bound) each_logit<TH>(buf, p, tid, edge, [&](float x, int) { mine += x >= bound; });
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int before = __shfl_up_sync(kFull, upto, o);
-            if (lane >= o) upto += before;
+                                       float edge, float top, int lane, int k) {
+    constexpr int kCap = TopShared<32>::kCap, kPer = Elem<T>::kPer;
+    const uint32_t q[1] = {order_of(top)};
+    const float bound = bound_of(q, k);
+    const unsigned below = (1u << lane) - 1u;
+    uint16_t* vectors = reinterpret_cast<uint16_t*>(sh.last);  // kCap of them
+    int nv = 0;
+    for (int base = 0; base < p.nv; base += 32) {
+        const int i = base + lane;
+        bool hit = false;
+        if (i < p.nv) {
+            const uint4 v = buf[i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            hit = vector_max<T>(w) >= bound;
         }
-        int at = 0;
-        if (lane == 31) at = atomicAdd(&sh.count, upto);
-        at = __shfl_sync(kFull, at, 31) + upto - mine;
-        if (mine)
-            each_logit<TH>(buf, p, tid, edge, [&](float x, int id) {
-                if (x >= bound) {
-                    if (at < kCap) sh.list[at] = key_of(x, id);
-                    ++at;
-                }
-            });
+        const unsigned hits = __ballot_sync(kFull, hit);
+        if (hit && nv + __popc(hits & below) < kCap) vectors[nv + __popc(hits & below)] = (uint16_t)i;
+        nv += __popc(hits);
     }
-    group_sync<TH>();
-    return sh.count;
+    if (nv > kCap) return kCap + 1;
+    __syncwarp();
+    int n = 0;
+    auto keep = [&](float x, int id, bool any) {
+        const bool hit = any && x >= bound;
+        const unsigned hits = __ballot_sync(kFull, hit);
+        const int at = n + __popc(hits & below);
+        if (hit && at < kCap) sh.list[at] = key_of(x, id);
+        n += __popc(hits);
+    };
+    const T* logits = reinterpret_cast<const T*>(buf);
+    for (int base = 0; base < nv * kPer; base += 32) {
+        const int e = base + lane;
+        const bool any = e < nv * kPer;
+        const int at = any ? vectors[e / kPer] * kPer + e % kPer : 0;
+        keep(any ? widen(logits[at]) : 0.f, p.first + at, any);
+    }
+    const int ie = p.edge(lane);
+    keep(edge, ie, ie >= 0);
+    __syncwarp();
+    return n;
 }
 
 // put(place, key) for the k largest of the list's n keys, and nothing for places past n.
@@ -368,7 +395,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
 // Longer rows: 128 threads a row, or the CTAs of a cluster where rows are few. A thread copies
 // and reads its own places of a ring of kStages chunks of kU vectors a thread; copies run
 // kStages - 1 chunks ahead, across rows.
-constexpr int kLong = 128, kU = 4, kStages = 3, kChunk = kU * kLong, kRemember = 16;
+constexpr int kLong = 128, kU = 4, kStages = 3, kChunk = kU * kLong, kRemember = 8;
 
 template <typename T, bool kTop>
 __global__ void __launch_bounds__(kLong, blocks_of<kLong>())
@@ -377,7 +404,7 @@ __global__ void __launch_bounds__(kLong, blocks_of<kLong>())
     extern __shared__ uint4 ring[];  // [kStages][kU][TH], then TopLists in a cluster
     __shared__ Joint<TH> joint;
     __shared__ TopShared<kTop ? TH : 32> tops;
-    __shared__ float of_chunk[kTop ? kRemember : 1][TH];  // threads' maxima of chunks c, c + 16, ...
+    __shared__ float of_chunk[kTop ? kRemember : 1][TH];  // threads' maxima of chunks c, c + 8, ...
     TopLists& lists = *reinterpret_cast<TopLists*>(ring + kStages * kChunk);
     const int tid = threadIdx.x;
     const int lc = in.log_cluster, cluster = 1 << lc;
@@ -527,7 +554,7 @@ __global__ void __launch_bounds__(kLong, blocks_of<kLong>())
         int n = 0;
         const uint4* vectors = reinterpret_cast<const uint4*>(p.x + p.first);
         if constexpr (kTop) {
-            if (tid < 32) find_bound(tops, top, tid, o.k);
+            if (tid < 32) find_bound(tops, tid, o.k);
             __syncthreads();
             const float bound = tops.bound;
             if (top >= bound) {  // its logits that reach it, from the chunks whose maximum does
@@ -709,10 +736,10 @@ cudaError_t forward_of(int threads, const RowsIn& in, const TokensIn& tk, const 
                        cudaStream_t s) {
     constexpr int kShort = kTop ? 32 : 16;
     if (threads == kShort)  // the last figures: static shared memory, rounded up
-        return launch_rows<&k_logprob<T, kShort, kTop>, kShort, 0>(in, kTop ? 5 * 1024 : 512, s, in, tk, o);
+        return launch_rows<&k_logprob<T, kShort, kTop>, kShort, 0>(in, kTop ? 6 * 1024 : 512, s, in, tk, o);
     RowsIn with_ring = in;
     with_ring.slots = kStages * kChunk + (kTop && in.log_cluster ? (int)sizeof(TopLists) / 16 + 1 : 0);
-    return launch_rows<&k_logprob_long<T, kTop>, kLong, 0>(with_ring, kTop ? 14 * 1024 : 1024, s, with_ring, tk, o);
+    return launch_rows<&k_logprob_long<T, kTop>, kLong, 0>(with_ring, kTop ? 8 * 1024 : 1024, s, with_ring, tk, o);
 }
 
 template <typename T>
