@@ -226,12 +226,13 @@ __device__ __forceinline__ int collect(TopShared<32>& sh, const Part<T>& p, cons
     return n;
 }
 
-// put(place, key) for the k largest of the list's n keys, and nothing for places past n.
-template <int TH, typename Put>
+// put(place, key) for the k largest of the list's n keys, and nothing for places past n; by G
+// threads together (a warp or the group).
+template <int G, int TH, typename Put>
 __device__ __forceinline__ void order_list(TopShared<TH>& sh, int n, int tid, int k, Put&& put) {
     if (tid < 8) sh.list[n + tid] = 0;  // a round number to count
-    group_sync<TH>();
-    for (int i = tid; i < n; i += TH) {
+    group_sync<G>();
+    for (int i = tid; i < n; i += G) {
         const Key key = sh.list[i];
         int place = 0;
         for (int l = 0; l < n; l += 8)
@@ -289,10 +290,14 @@ __device__ __forceinline__ void put_top(TopShared<TH>& sh, const ValuesOut& o, i
         if (lps != nullptr)
             lps[place] = broken ? NAN : key ? log_prob(key_value(key), c, m, ln_s) : -kInf;
     };
-    if (broken) n = 0;
-    else if (over) n = take_rounds<TH>(sh, p, buf, edge, tid, o.k, out);
-    else order_list(sh, n, tid, o.k, out);
-    for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
+    if (over && !broken) {
+        n = take_rounds<TH>(sh, p, buf, edge, tid, o.k, out);
+        for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
+    } else if (tid < 32) {  // a CTA's other warps go on
+        if (broken) n = 0;
+        else order_list<32>(sh, n, tid, o.k, out);
+        for (int i = n + tid; i < o.k; i += 32) out(i, Key(0));
+    }
 }
 
 // The same from the lists that the cluster's CTAs gave.
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
 constexpr int kLong = 128, kU = 4, kStages = 3, kChunk = kU * kLong, kRemember = 8;
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLong, blocks_of<kLong>())
+__global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
     k_logprob_long(RowsIn in, TokensIn tk, ValuesOut o) {
     constexpr int TH = kLong, kPer = Elem<T>::kPer, kPairs = kPer / 2;
     extern __shared__ uint4 ring[];  // [kStages][kU][TH], then TopLists in a cluster
@@ -557,26 +562,29 @@ __global__ void __launch_bounds__(kLong, blocks_of<kLong>())
             if (tid < 32) find_bound(tops, tid, o.k);
             __syncthreads();
             const float bound = tops.bound;
-            if (top >= bound) {  // its logits that reach it, from the chunks whose maximum does
+            if (__any_sync(kFull, top >= bound)) {
+                // the logits that reach it, from the chunks whose maximum does: each lane goes
+                // through its own, so that the lanes' loads travel together
                 auto keep = [&](float x, int id) {
                     if (x < bound) return;
                     const int at = atomicAdd(&tops.count, 1);
                     if (at < TopShared<TH>::kCap) tops.list[at] = key_of(x, id);
                 };
-                for (int c = 0; c < chunks; ++c) {
-                    if (of_chunk[c % kRemember][tid] < bound) continue;
+                for (int c = top >= bound ? 0 : chunks;; ++c) {
+                    while (c < chunks && of_chunk[c % kRemember][tid] < bound) ++c;
+                    if (!__any_sync(kFull, c < chunks)) break;
+                    const int first = c * kChunk + tid;
                     uint4 q[kU];
 #pragma unroll
                     for (int u = 0; u < kU; ++u) {
-                        const int i = c * kChunk + u * TH + tid;
                         q[u] = make_uint4(Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill);
-                        if (i < p.nv) q[u] = vectors[i];
+                        if (c < chunks && first + u * TH < p.nv) q[u] = vectors[first + u * TH];
                     }
 #pragma unroll
                     for (int u = 0; u < kU; ++u) {
                         const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
                         if (vector_max<T>(w) < bound) continue;
-                        const int id = p.first + (c * kChunk + u * TH + tid) * kPer;
+                        const int id = p.first + (first + u * TH) * kPer;
 #pragma unroll
                         for (int j = 0; j < kPer; ++j) keep(element<T>(w, j), id + j);
                     }
@@ -596,7 +604,7 @@ __global__ void __launch_bounds__(kLong, blocks_of<kLong>())
                 if (n > TopShared<TH>::kCap) {
                     n = take_rounds<TH>(tops, p, vectors, edge, tid, o.k, give);
                 } else if (n > o.k) {
-                    order_list(tops, n, tid, o.k, give);
+                    order_list<TH>(tops, n, tid, o.k, give);
                     n = o.k;
                 } else {
                     for (int i = tid; i < n; i += TH) give(i, tops.list[i]);
