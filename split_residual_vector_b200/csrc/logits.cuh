@@ -458,10 +458,12 @@ __device__ __forceinline__ Stats join_lanes(float m, float s, float w, float c2)
     return r;
 }
 
-template <int TH>
+// The barrier of N threads: those of a group, or of the whole CTA. Warps with different work may
+// meet here from different places.
+template <int N>
 __device__ __forceinline__ void group_sync() {
-    if constexpr (TH <= 32) __syncwarp(lane_mask<TH>());
-    else __syncthreads();
+    if constexpr (N <= 32) __syncwarp(lane_mask<N>());
+    else asm volatile("barrier.sync 1, %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -488,17 +490,18 @@ struct Joint {
     float cta[2][3][kMaxCluster];
 };
 
-// The group's statistics in every thread of it. Contains the group's barrier (before it, threads
-// may leave what the others need after it in shared memory).
-template <int TH, bool kW>
+// The group's statistics in every thread of it, and of the N - TH threads beside it (which only
+// read). Contains the barrier of all N (before it, threads may leave what the others need after it
+// in shared memory).
+template <int TH, bool kW, int N = TH>
 __device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, int parity, float c2) {
-    // threads past TH only read
     st.s = lanes_sum<TH>(st.s);
     if constexpr (kW) st.w = lanes_sum<TH>(st.w);
     if constexpr (TH <= 32) {
         group_sync<TH>();
         return st;
     } else {
+        static_assert(N % 32 == 0, "whole warps");
         const int lane = tid & 31;
         float(&at)[3][(TH + 31) / 32] = j.warp[parity];
         if (lane == 0 && tid < TH) {
@@ -506,7 +509,7 @@ __device__ __forceinline__ Stats join_group(Joint<TH>& j, Stats st, int tid, int
             at[1][tid / 32] = st.s;
             if constexpr (kW) at[2][tid / 32] = st.w;
         }
-        group_sync<TH>();
+        group_sync<N>();
         const bool in = lane < TH / 32;
         return join_lanes<kW>(in ? at[0][lane] : -kInf, in ? at[1][lane] : 0.f,
                               kW && in ? at[2][lane] : 0.f, c2);
@@ -533,10 +536,10 @@ __device__ __forceinline__ Stats join_cluster(const Joint<TH>& j, int tid, int c
 }
 
 // The row's statistics in every thread of every CTA that shares it.
-template <int TH, bool kW>
+template <int TH, bool kW, int N = TH>
 __device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int cluster, int rank,
                                           int parity, float c2) {
-    st = join_group<TH, kW>(j, st, tid, parity, c2);
+    st = join_group<TH, kW, N>(j, st, tid, parity, c2);
     if (cluster > 1) {
         if (tid < cluster) push_stats<TH, kW>(j, st, rank, tid, parity);
         cluster_sync();

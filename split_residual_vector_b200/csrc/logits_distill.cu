@@ -35,10 +35,11 @@ struct TeacherIn {
     unsigned long long* n_bad;
 };
 
-// A place of the list: the lister's lane l has places l, l + lanes, ...
-struct alignas(16) Entry {
-    int id;          // -1: an empty place
-    float q, lq, x;  // weight, its logarithm, the student's logit
+// A place of the list; the lister's lane l has places l, l + lanes, ... in registers, and what it
+// looks up of others here.
+struct Entry {
+    int id;   // -1 - place: an empty place
+    float q;  // weight (tail: first its logarithm)
 };
 
 // What the list leaves for the group.
@@ -67,12 +68,250 @@ __host__ __device__ constexpr int lister_of() { return TH > 32 ? 32 : 0; }
 template <int TH>
 __host__ __device__ constexpr int distill_blocks() { return 1024 / (block_of<TH>() + lister_of<TH>()); }
 
+// A row's statistics when the rest's and the listed logits' are joined.
+struct Whole {
+    Stats rest, all;
+    float Q, qr;  // sum of the weights, the tail's weight
+    bool empty;
+    __device__ __forceinline__ bool none(float g) const { return g == 0.f || empty || all.s == 0.f; }
+};
+
+// The list of a row, kept in registers by the lanes of its lister: lane l has places l, l + L, ...
+template <typename T, int TH>
+struct Lister {
+    static constexpr int L = lanes_of<TH>(), kLane = (TH <= 32 ? kShortTop : kMaxTop) / L;
+    using B = Bits<T>;
+    int id[kLane];  // below 0: an empty place
+    float q[kLane], lq[kLane], x[kLane];  // weight, its logarithm, the student's logit
+    // bit i of `mine`: place me + L i is in this share, of `first`: and the first of its id
+    unsigned mine, first;
+    float tmax;
+    bool broken, twice, some;  // NaN or +inf in an entry, an id listed twice, any entry
+    int next_id[kLane];  // the next row's
+    float next_t[kLane];
+
+    template <typename F>
+    __device__ __forceinline__ static void each(int k, F&& f) {
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) {
+            if (i * L >= k) break;
+            f(i);
+        }
+    }
+    // sends for a row's list
+    __device__ __forceinline__ void load(const TeacherIn& te, int64_t r, int me) {
+        const int64_t at = r * te.k;
+        each(te.k, [&](int i) {
+            const int e = me + L * i;
+            next_id[i] = -1;
+            next_t[i] = -kInf;
+            if (e < te.k) {
+                next_id[i] = __ldg(te.ids + at + e);
+                next_t[i] = te.t_bf16 ? widen(__ldg(static_cast<const __nv_bfloat16*>(te.t) + at + e))
+                                      : __ldg(static_cast<const float*>(te.t) + at + e);
+            }
+        });
+    }
+    // takes the list that was sent for; what can be known of it without the row
+    __device__ __forceinline__ void take(const TeacherIn& te, const Part<T>& p, int rank, int me,
+                                         Entry* list) {
+        const unsigned mask = lane_mask<TH>();
+        int n = 0, bad = 0;
+        mine = first = 0;
+        tmax = -kInf;
+        broken = twice = false;
+        __syncwarp(mask);  // the last row's list has been read
+        each(te.k, [&](int i) {
+            const int e = me + L * i, given = next_id[i];
+            bad += given >= p.V;
+            id[i] = given >= 0 && given < p.V ? given : -1 - e;
+            const bool there = id[i] >= 0;
+            lq[i] = there ? next_t[i] : -kInf;
+            q[i] = 0.f;
+            x[i] = -kInf;
+            n += there;
+            tmax = fmaxf(tmax, lq[i]);
+            broken |= !(lq[i] < kInf);
+            if (e < te.k) list[e] = Entry{id[i], lq[i]};
+            const unsigned same = __match_any_sync(mask, id[i]);
+            bool again = (same & ((1u << (threadIdx.x & 31)) - 1u)) != 0;
+            if (i) {
+                __syncwarp(mask);
+                for (int l = 0; l < i * L; ++l) again |= list[l].id == id[i];
+            }
+            again &= there;
+            twice |= again;
+            if (there && (p.place(id[i]) >= 0 || (rank == 0 && p.in_edges(id[i])))) {
+                mine |= 1u << i;
+                if (!again) first |= 1u << i;
+            }
+        });
+        twice = __any_sync(mask, twice);
+        if (bad && rank == 0 && te.n_bad != nullptr)
+            atomicAdd(te.n_bad, (unsigned long long)bad);
+        tmax = lanes_max<TH>(tmax);
+        broken = __any_sync(mask, broken);
+        some = __any_sync(mask, n > 0);
+    }
+    __device__ __forceinline__ bool empty(const TeacherIn& te) const {
+        return !some || (!te.tail && tmax == -kInf && !broken);
+    }
+    // reads the listed elements of this share and hides them
+    __device__ __forceinline__ void hide(const TeacherIn& te, const Part<T>& p, uint4* buf, T* edge,
+                                         bool others) {
+        auto cell = [&](int i) {
+            const int at = p.place(id[i]);
+            return at >= 0 ? reinterpret_cast<B*>(buf) + at
+                           : reinterpret_cast<B*>(edge) + p.edge_lane(id[i]);
+        };
+        each(te.k, [&](int i) {
+            if ((mine >> i) & 1u) {
+                B* at = cell(i);
+                x[i] = widen(*reinterpret_cast<const T*>(at));
+                if (!twice) *at = (B)Elem<T>::kFill;
+            } else if (others && id[i] >= 0) {
+                x[i] = widen(p.x[id[i]]);  // another CTA's; for the loss
+            }
+        });
+        if (twice) {
+            __syncwarp(lane_mask<TH>());
+            each(te.k, [&](int i) {
+                if ((mine >> i) & 1u) *cell(i) = (B)Elem<T>::kFill;
+            });
+        }
+    }
+    // the weights, and this share's listed logits, for the group
+    __device__ __forceinline__ void weigh(const TeacherIn& te, int me, Entry* list,
+                                          ListShared<T>& ls, float c2) {
+        float Q = 1.f, tail_q = 0.f;
+        if (te.tail) {
+            // the tail's weight is what the list leaves of 1: in float64, or a tail of 1e-6 would
+            // be rounding
+            double sum = 0.0;
+#pragma unroll 1
+            for (int e = me; e < te.k; e += L)
+                if (list[e].id >= 0) sum += exp((double)list[e].q);
+            sum = lanes_sum<TH>(sum);
+            Q = broken ? NAN : (float)sum;
+            tail_q = (float)fmax(0.0, 1.0 - sum);
+        } else {
+            const float tm = tmax == -kInf ? 0.f : tmax;
+            float sum = 0.f;
+            each(te.k, [&](int i) {
+                lq[i] -= tm;
+                if (id[i] >= 0) sum += expf(lq[i]);
+            });
+            sum = lanes_sum<TH>(sum);
+            if (broken) Q = NAN;
+            const float ln_sum = logf(sum);
+            each(te.k, [&](int i) { lq[i] -= ln_sum; });
+        }
+        float m = -kInf, sum = 0.f;
+        each(te.k, [&](int i) {
+            if (id[i] >= 0) q[i] = expf(lq[i]);
+            if ((first >> i) & 1u) m = fmaxf(m, x[i]);
+        });
+        m = lanes_max<TH>(m);
+        each(te.k, [&](int i) {
+            if ((first >> i) & 1u) sum += ex2(exponent(x[i], m, c2));
+        });
+        sum = lanes_sum<TH>(sum);
+        if (twice) {
+            each(te.k, [&](int i) {
+                if (me + L * i < te.k) list[me + L * i].q = q[i];
+            });
+            __syncwarp(lane_mask<TH>());
+        }
+        if (me == 0) {
+            ls.m = m;
+            ls.s = sum;
+            ls.Q = Q;
+            ls.tail_q = tail_q;
+        }
+    }
+    __device__ __forceinline__ void put_loss(const TeacherIn& te, int64_t r, int me, const Whole& w,
+                                             float c) const {
+        const float ln_s = ln(w.all.s);
+        float part = 0.f;
+        if (!w.empty) {
+            each(te.k, [&](int i) {
+                if (id[i] >= 0 && q[i] != 0.f)
+                    part += q[i] * (lq[i] - (w.all.s == 0.f ? -kInf : log_prob(x[i], c, w.all.m, ln_s)));
+            });
+            part = lanes_sum<TH>(part);
+            if (w.qr > 0.f)
+                part += w.qr * (logf(w.qr) - (c * (w.rest.m - w.all.m) + ln(w.rest.s) - ln_s));
+        }
+        if (me == 0) te.loss[r] = w.Q != w.Q ? NAN : part;
+    }
+    // the listed tokens' gradients, over the rest's
+    __device__ __forceinline__ void put_listed(const TeacherIn& te, const Whole& w, float gc,
+                                               float c2, const Entry* list, T* d) const {
+        const float inv = reciprocal(w.all.s);
+        each(te.k, [&](int i) {
+            if (!((first >> i) & 1u)) return;
+            float weight = q[i];
+            if (twice) {
+                weight = 0.f;
+                for (int l = 0; l < te.k; ++l)
+                    if (list[l].id == id[i]) weight += list[l].q;
+            }
+            const float pi = ex2(exponent(x[i], w.all.m, c2)) * inv;
+            narrow(gc * (w.Q * pi - weight), d + id[i]);
+        });
+    }
+};
+
+// The unlisted tokens' gradients of a share.
+template <int TH, typename T>
+__device__ __forceinline__ void put_rest(const Part<T>& p, const uint4* buf, int tid, int ie,
+                                         float edge, const Whole& w, bool none, float gc, float c2,
+                                         T* d) {
+    constexpr int kPer = Part<T>::kPer;
+    const bool wide = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(p.x)) & 15u) == 0;
+    T* out = d + p.first;
+    if (none) {
+        for (int i = tid; i < p.nv; i += TH) {
+            const float y[kPer] = {};
+            store_vector<T>(out + (size_t)i * kPer, wide, y);
+        }
+        if (ie >= 0) narrow(0.f, d + ie);
+        return;
+    }
+    const Scale k(c2, w.rest.m);
+    // a rest of -inf only has no gradient of its own: 2^t is 0 there
+    const float f0 = gc * (w.Q * reciprocal(w.all.s)
+                               * (w.rest.s == 0.f ? 1.f : ex2((w.rest.m - w.all.m) * c2))
+                           - (w.qr > 0.f ? w.qr / w.rest.s : 0.f));
+    const bool fast = !k.far && wide;
+    const float f = fast ? f0 * ex2(-k.shift) : f0;
+    auto put = [&](int i, const Pair (&t)[kPer / 2], bool whole) {
+        float y[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e)
+            halves(mul2(ex2_pair(t[e]), pair_of(f, f)), y[2 * e], y[2 * e + 1]);
+        store_vector<T>(out + (size_t)i * kPer, whole, y);
+    };
+    if (fast)
+        each_vector<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&v)[4]) {
+            Pair t[kPer / 2];
+            exponents<T, false, false>(v, k, t);
+            put(i, t, true);
+        });
+    else
+        each_in_turn<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&v)[4]) {
+            Pair t[kPer / 2];
+            exponents<T, false, true>(v, k, t);
+            put(i, t, wide);
+        });
+    if (ie >= 0) narrow(ex2(exponent(edge, w.rest.m, c2)) * f0, d + ie);
+}
+
+// kGrad: the gradient, with the losses where they are wanted; else the losses.
 template <typename T, int TH, bool kGrad>
 __global__ void __launch_bounds__(block_of<TH>() + lister_of<TH>(), distill_blocks<TH>())
     k_distill(RowsIn in, TeacherIn te) {
-    constexpr int kRows = block_of<TH>() / TH, kPer = Part<T>::kPer;
-    constexpr int L = lanes_of<TH>(), kLane = (TH <= 32 ? kShortTop : kMaxTop) / L;
-    using B = Bits<T>;
+    constexpr int kRows = block_of<TH>() / TH, N = TH + lister_of<TH>();
     extern __shared__ uint4 buffers[];  // [groups][slots]: the row's vectors, then the list
     __shared__ Joint<TH> joint[kRows];
     __shared__ ListShared<T> lists[kRows];
@@ -81,295 +320,173 @@ __global__ void __launch_bounds__(block_of<TH>() + lister_of<TH>(), distill_bloc
     const int group = TH > 32 ? 0 : group_in_block<TH>();
     const int lc = TH <= 32 ? 0 : in.log_cluster, cluster = 1 << lc;
     const int rank = lc ? (int)cluster_ctarank() : 0;
-    const bool worker = tid < TH, first_lanes = rank == 0 && tid < L;  // the latter have the edges
-    const bool lister = TH <= 32 || !worker;
-    const int me = TH <= 32 ? tid : tid - TH;  // the lister's lane
-    const unsigned mask = lane_mask<TH>();
+    const bool first_lanes = rank == 0 && tid < lanes_of<TH>();  // have the row's edges
     uint4* buf = buffers + (size_t)group * in.slots;
-    Entry* list = reinterpret_cast<Entry*>(buf + in.slots - te.k);
+    Entry* list = reinterpret_cast<Entry*>(buf + in.slots - (te.k + 1) / 2);
     const float c2 = in.c * kLog2e;
     ListShared<T>& ls = lists[group];
+    Joint<TH>& jt = joint[group];
     if (lc) cluster_sync();  // every CTA runs before one writes to another
     RowWalk row((int64_t)(blockIdx.x >> lc) * kRows + group,
                 (int64_t)(gridDim.x >> lc) * kRows, in.n);
     if (row.r >= in.rows) return;
-    // the row's weight and list: loaded a row ahead
-    float g_next = 1.f;
-    int id_next[kLane];
-    float t_next[kLane];
-    auto list_at = [&]() {
-        if (row.r >= in.rows) return;
-        if (kGrad && te.g != nullptr) g_next = __ldg(te.g + row.r);
-        if (lister) {
-            const int64_t at = row.r * te.k;
-#pragma unroll
-            for (int i = 0; i < kLane; ++i) {
-                if (i * L >= te.k) break;
-                const int e = me + L * i;
-                id_next[i] = -1;
-                if (e < te.k) {
-                    id_next[i] = __ldg(te.ids + at + e);
-                    t_next[i] = te.t_bf16 ? widen(__ldg(static_cast<const __nv_bfloat16*>(te.t) + at + e))
-                                          : __ldg(static_cast<const float*>(te.t) + at + e);
-                }
-            }
+    auto part_at = [&]() {
+        return Part<T>(static_cast<const T*>(in.x) + row.s * in.ss + row.j * in.sn, in.V, rank, lc);
+    };
+    auto weight_at = [&]() {
+        return kGrad && te.g != nullptr && row.r < in.rows ? __ldg(te.g + row.r) : 1.f;
+    };
+    // a gradient of weight 0 alone: zeros, whatever the row is
+    auto skipped = [&](float g) { return kGrad && g == 0.f && te.loss == nullptr; };
+    auto gradient_at = [&](const RowWalk& w) {
+        return static_cast<T*>(te.d) + w.s * te.d_ss + w.j * te.d_sn;
+    };
+    int parity = 0;
+    // the row's joined statistics, behind the barrier that the lister and the row's threads share
+    auto join = [&](Stats rest) {
+        Whole w;
+        w.empty = false;
+        w.rest = join_row<TH, false, N>(jt, rest, tid, cluster, rank, parity, c2);
+        float lm = ls.m, lsum = ls.s;
+        if (lc) {
+            const int lane = tid & 31;
+            const bool in_c = lane < cluster;
+            const Stats l = join_lanes<false>(in_c ? listed_of.cta[parity][0][lane] : -kInf,
+                                              in_c ? listed_of.cta[parity][1][lane] : 0.f, 0.f, c2);
+            lm = l.m;
+            lsum = l.s;
         }
+        parity ^= 1;
+        w.all = Stats{fmaxf(w.rest.m, lm), 0.f, 0.f};
+        const float mu = w.all.m == -kInf ? 0.f : w.all.m;
+        w.all.s = w.rest.s * ex2((w.rest.m - mu) * c2) + lsum * ex2((lm - mu) * c2);
+        w.qr = w.rest.s == 0.f ? 0.f : ls.tail_q;
+        w.Q = te.tail ? ls.Q + w.qr : ls.Q;
+        return w;
     };
-    // a row's part of what is read for it: its share of the vectors, and an element beside them
-    struct At {
-        Part<T> p;
-        int64_t r, s;
-        int j, ie;
-        float g, edge;
-        bool skip;  // a gradient of weight 0 alone: zeros, whatever the row is
-    };
-    auto at_row = [&]() {
-        At at{Part<T>(static_cast<const T*>(in.x) + row.s * in.ss + row.j * in.sn, in.V, rank, lc),
-              row.r, row.s, row.j, -1, kGrad ? g_next : 1.f, -kInf, false};
-        at.skip = kGrad && at.g == 0.f && te.loss == nullptr;
-        at.ie = first_lanes ? at.p.edge(tid) : -1;
-        if (!at.skip && at.ie >= 0) at.edge = widen(at.p.x[at.ie]);
-        return at;
-    };
-    list_at();
-    At now = at_row();
-    if (!now.skip && worker) fetch<TH>(buf, now.p, tid);
-    for (int parity = 0;;) {
-        const Part<T> p = now.p;
-        const int64_t r = now.r;
-        const int ie = now.ie;
-        const float g = now.g;
-        float edge = now.edge;
-        const bool skip = now.skip;
-        T* d = static_cast<T*>(te.d) + now.s * te.d_ss + now.j * te.d_sn;
-        const bool wide = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(p.x)) & 15u) == 0;
-        T* out = d + p.first;
-        int n = 0, bad = 0;
-        float tmax = -kInf;
-        bool broken = false;  // NaN or +inf among the entries
-        unsigned first = 0;   // bit i: entry me + L i is this share's, the first of its id
-        bool twice = false;   // some id is listed twice
-        if (lister) {
-            __syncwarp(mask);  // the last row's list has been read
-#pragma unroll
-            for (int i = 0; i < kLane; ++i) {
-                if (i * L >= te.k) break;
-                const int e = me + L * i;
-                int id = -1 - e;  // empty places differ
-                if (e < te.k) {
-                    const int given = id_next[i];
-                    bad += given >= in.V;
-                    if (given >= 0 && given < in.V) id = given;
-                    const float t = id >= 0 ? t_next[i] : -kInf;
-                    n += id >= 0;
-                    tmax = fmaxf(tmax, t);
-                    broken |= !(t < kInf);
-                    list[e].id = id < 0 ? -1 : id;
-                    list[e].lq = t;
+    const Whole nothing{{-kInf, 0.f, 0.f}, {-kInf, 0.f, 0.f}, 0.f, 0.f, true};
+    const Stats no_rest{-kInf, 0.f, 0.f};
+
+    if (TH > 32 && tid >= TH) {  // ---- the lister
+        const int me = tid - TH;
+        Lister<T, TH> lister;
+        lister.load(te, row.r, me);
+        float g_next = weight_at();
+        while (true) {
+            const Part<T> p = part_at();
+            const int64_t r = row.r;
+            T* d = gradient_at(row);
+            const float g = g_next;
+            lister.take(te, p, rank, me, list);
+            row.next(in.n);
+            const bool more = row.r < in.rows;
+            if (more) lister.load(te, row.r, me);
+            g_next = weight_at();
+            Whole w = nothing;
+            if (!skipped(g)) {
+                group_sync<N>();  // the row is here
+                lister.hide(te, p, buf, ls.edge, lc != 0 && rank == 0);
+                const bool empty = lister.empty(te);
+                if (me == 0) ls.empty = empty;
+                group_sync<N>();  // the listed tokens are hidden
+                if (!empty) {
+                    lister.weigh(te, me, list, ls, c2);
+                    __syncwarp();
+                    if (lc && me < cluster) {
+                        const uint32_t to = cluster_map(smem_u32(&listed_of.cta[parity][0][rank]), me);
+                        st_cluster_f32(to, ls.m);
+                        st_cluster_f32(to + 4 * kMaxCluster, ls.s);
+                    }
+                    w = join(no_rest);
                 }
-                const unsigned same = __match_any_sync(mask, id);
-                bool again = id >= 0 && (same & ((1u << (threadIdx.x & 31)) - 1u));
-                __syncwarp(mask);
-                for (int l = 0; l < i * L; ++l) again |= id >= 0 && list[l].id == id;
-                twice |= again;
-                if (id >= 0 && !again && (p.place(id) >= 0 || (rank == 0 && p.in_edges(id))))
-                    first |= 1u << i;
+                if (te.loss != nullptr && rank == 0) lister.put_loss(te, r, me, w, in.c);
             }
-            twice = __any_sync(mask, twice);
-            if (bad && rank == 0 && te.n_bad != nullptr)
-                atomicAdd(te.n_bad, (unsigned long long)bad);
-            tmax = lanes_max<TH>(tmax);
-            broken = __any_sync(mask, broken);
-            n = __any_sync(mask, n > 0);
+            if (kGrad && !w.none(g)) {
+                group_sync<N>();  // the listed tokens' places hold the rest's gradient by now
+                lister.put_listed(te, w, g * in.c, c2, list, d);
+            }
+            if (!more) break;
         }
+        return;
+    }
+
+    // ---- the row's threads; half a warp's row lists for itself
+    Lister<T, 16> own;
+    float g_next = weight_at();
+    if constexpr (TH <= 32) own.load(te, row.r, tid);
+    Part<T> p = part_at();
+    float edge = -kInf;
+    int ie = -1;
+    auto send = [&]() {  // for the row's vectors, and the element beside them
+        ie = first_lanes ? p.edge(tid) : -1;
+        edge = -kInf;
+        if (skipped(g_next)) return;
+        fetch<TH>(buf, p, tid);
+        if (ie >= 0) edge = widen(p.x[ie]);
+    };
+    send();
+    while (true) {
+        const int64_t r = row.r;
+        T* d = gradient_at(row);
+        const float g = g_next;
+        if constexpr (TH <= 32) own.take(te, p, 0, tid, list);
         row.next(in.n);
         const bool more = row.r < in.rows;
-        list_at();
-        bool empty = true;
-        if (!skip) {
-            arrived();
-            if (first_lanes && tid < 16 && ie >= 0) narrow(edge, &ls.edge[tid]);
-            group_sync<TH>();  // the row is here
-            if (lister) {
-                // the listed elements of this share: read, then hidden
-                auto each = [&](auto&& f) {
-                    for (int e = me, i = 0; e < te.k; e += L, ++i) {
-                        const int id = list[e].id, q = p.place(id);
-                        if (id < 0 || (q < 0 && (rank != 0 || !p.in_edges(id)))) continue;
-                        f(e, q >= 0 ? reinterpret_cast<B*>(buf) + q
-                                    : reinterpret_cast<B*>(ls.edge) + p.edge_lane(id));
-                    }
-                };
-                auto read = [&](int e, B* at) { list[e].x = widen(*reinterpret_cast<const T*>(at)); };
-                auto hide = [&](int, B* at) { *at = (B)Elem<T>::kFill; };
-                if (!twice) {
-                    each([&](int e, B* at) {
-                        read(e, at);
-                        hide(e, at);
-                    });
-                } else {
-                    each(read);
-                    __syncwarp(mask);
-                    each(hide);
-                }
-                if (lc && rank == 0)  // other CTAs' elements; for the loss
-                    for (int e = me; e < te.k; e += L) {
-                        const int id = list[e].id;
-                        if (id >= 0 && p.place(id) < 0 && !p.in_edges(id)) list[e].x = widen(p.x[id]);
-                    }
-                if (me == 0) ls.empty = !n || (!te.tail && tmax == -kInf && !broken);
-            }
-            group_sync<TH>();  // the listed tokens are hidden
-            if (ie >= 0) edge = widen(ls.edge[tid]);
-            empty = ls.empty != 0;
+        if constexpr (TH <= 32)
+            if (more) own.load(te, row.r, tid);
+        g_next = weight_at();
+        Whole w = nothing;
+        const int here = ie;
+        float beside = edge;
+        Next<T> next{buf, nullptr, 0};
+        Part<T> coming = p;
+        if (!kGrad && more) {  // losses read the row once: places are refilled as they are read
+            coming = part_at();
+            next = Next<T>{buf, coming.x + coming.first, coming.nv};
         }
-        if (more) now = at_row();
-        const Next<T> next{buf, now.p.x + now.p.first, more && !now.skip ? now.p.nv : 0};
-        Stats rest{-kInf, 0.f, 0.f}, all{-kInf, 0.f, 0.f};
-        if (!empty) {
-            if (worker) {
+        int refilled = 0;
+        if (!skipped(g)) {
+            arrived();
+            if (here >= 0) narrow(beside, &ls.edge[tid]);
+            group_sync<N>();  // the row is here
+            bool empty;
+            if constexpr (TH <= 32) {
+                own.hide(te, p, buf, ls.edge, false);
+                empty = own.empty(te);
+                group_sync<N>();
+            } else {
+                group_sync<N>();  // the listed tokens are hidden
+                empty = ls.empty != 0;
+            }
+            if (here >= 0) beside = widen(ls.edge[tid]);
+            if (!empty) {
                 float top;
-                rest = pass<TH, false, T>(buf, p.nv, tid, edge, c2, top, [&](int i) {
+                const Stats rest = pass<TH, false, T>(buf, p.nv, tid, beside, c2, top, [&](int i) {
                     if (!kGrad) next.refill(i);
                 });
+                refilled = p.nv;
+                if constexpr (TH <= 32) own.weigh(te, tid, list, ls, c2);
+                w = join(rest);
             }
-            if (lister) {  // the weights and this share's listed logits
-                float Q = 1.f, tail_q = 0.f;
-                if (te.tail) {
-                    // the tail's weight is what the list leaves of 1: in float64, or a tail of
-                    // 1e-6 would be rounding
-                    double sum = 0.0;
-                    for (int e = me; e < te.k; e += L) {
-                        const bool in_list = list[e].id >= 0;
-                        list[e].q = in_list ? expf(list[e].lq) : 0.f;
-                        if (in_list) sum += exp((double)list[e].lq);
-                    }
-                    sum = lanes_sum<TH>(sum);
-                    Q = broken ? NAN : (float)sum;
-                    tail_q = (float)fmax(0.0, 1.0 - sum);
-                } else {
-                    const float tm = tmax == -kInf ? 0.f : tmax;
-                    float sum = 0.f;
-                    for (int e = me; e < te.k; e += L)
-                        if (list[e].id >= 0) sum += expf(list[e].lq - tm);
-                    sum = lanes_sum<TH>(sum);
-                    if (broken) Q = NAN;
-                    const float ln_sum = logf(sum);
-                    for (int e = me; e < te.k; e += L) {
-                        const float lq = (list[e].lq - tm) - ln_sum;
-                        list[e].lq = lq;
-                        list[e].q = list[e].id >= 0 ? expf(lq) : 0.f;
-                    }
-                }
-                float m = -kInf, sum = 0.f;
-                for (int e = me, i = 0; e < te.k; e += L, ++i)
-                    if ((first >> i) & 1u) m = fmaxf(m, list[e].x);
-                m = lanes_max<TH>(m);
-                for (int e = me, i = 0; e < te.k; e += L, ++i)
-                    if ((first >> i) & 1u) sum += ex2(exponent(list[e].x, m, c2));
-                sum = lanes_sum<TH>(sum);
-                if (me == 0) {
-                    ls.m = m;
-                    ls.s = sum;
-                    ls.Q = Q;
-                    ls.tail_q = tail_q;
-                }
-                if (lc && me < cluster) {
-                    const uint32_t to = cluster_map(smem_u32(&listed_of.cta[parity][0][rank]), me);
-                    st_cluster_f32(to, m);
-                    st_cluster_f32(to + 4 * kMaxCluster, sum);
-                }
-            }
-            rest = join_row<TH, false>(joint[group], rest, tid, cluster, rank, parity, c2);
-            float lm = ls.m, lsum = ls.s;
-            if (lc) {
-                const int lane = tid & 31;
-                const bool in_c = lane < cluster;
-                const Stats l = join_lanes<false>(in_c ? listed_of.cta[parity][0][lane] : -kInf,
-                                                  in_c ? listed_of.cta[parity][1][lane] : 0.f, 0.f,
-                                                  c2);
-                lm = l.m;
-                lsum = l.s;
-            }
-            parity ^= 1;
-            all.m = fmaxf(rest.m, lm);
-            const float mu = all.m == -kInf ? 0.f : all.m;
-            all.s = rest.s * ex2((rest.m - mu) * c2) + lsum * ex2((lm - mu) * c2);
+            if constexpr (TH <= 32)
+                if (te.loss != nullptr) own.put_loss(te, r, tid, w, in.c);
         }
-        const bool none = g == 0.f || empty || all.s == 0.f;  // a gradient of zeros
-        float qr = 0.f, Q = 0.f;
-        if (!empty) {
-            qr = rest.s == 0.f ? 0.f : ls.tail_q;
-            Q = te.tail ? ls.Q + qr : ls.Q;
-        }
-        if (kGrad && worker) {
-            if (none) {
-                for (int i = tid; i < p.nv; i += TH) {
-                    const float y[kPer] = {};
-                    store_vector<T>(out + (size_t)i * kPer, wide, y);
-                }
-                if (ie >= 0) narrow(0.f, d + ie);
-            } else {
-                const float gc = g * in.c, inv = reciprocal(all.s);
-                const Scale k(c2, rest.m);
-                // a rest of -inf only has no gradient of its own: 2^t is 0 there
-                const float f0 = gc * (Q * inv * (rest.s == 0.f ? 1.f : ex2((rest.m - all.m) * c2))
-                                       - (qr > 0.f ? qr / rest.s : 0.f));
-                const bool fast = !k.far && wide;
-                const float f = fast ? f0 * ex2(-k.shift) : f0;
-                auto put = [&](int i, const Pair (&t)[kPer / 2], bool whole) {
-                    float y[kPer];
-#pragma unroll
-                    for (int e = 0; e < kPer / 2; ++e)
-                        halves(mul2(ex2_pair(t[e]), pair_of(f, f)), y[2 * e], y[2 * e + 1]);
-                    store_vector<T>(out + (size_t)i * kPer, whole, y);
-                };
-                if (fast)
-                    each_vector<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
-                        Pair t[kPer / 2];
-                        exponents<T, false, false>(w, k, t);
-                        put(i, t, true);
-                    });
-                else
-                    each_in_turn<TH>(buf, p.nv, tid, [&](int i, const uint32_t (&w)[4]) {
-                        Pair t[kPer / 2];
-                        exponents<T, false, true>(w, k, t);
-                        put(i, t, wide);
-                    });
-                if (ie >= 0) narrow(ex2(exponent(edge, rest.m, c2)) * f0, d + ie);
+        if constexpr (kGrad) {
+            const bool none = w.none(g);
+            put_rest<TH>(p, buf, tid, here, beside, w, none, g * in.c, c2, d);
+            if (more) {
+                p = part_at();
+                send();
             }
-        }
-        if (more && worker) next.template rest<TH>(kGrad || empty ? 0 : p.nv, tid);
-        if (te.loss != nullptr && lister && rank == 0) {
-            const float ln_s = ln(all.s);
-            float part = 0.f;
-            if (!empty) {
-                for (int e = me; e < te.k; e += L)
-                    if (list[e].id >= 0 && list[e].q != 0.f)
-                        part += list[e].q * (list[e].lq - (all.s == 0.f ? -kInf : log_prob(list[e].x, in.c, all.m, ln_s)));
-                part = lanes_sum<TH>(part);
-                if (qr > 0.f)
-                    part += qr * (logf(qr) - (in.c * (rest.m - all.m) + ln(rest.s) - ln_s));
+            if (!none) {
+                group_sync<N>();  // the listed tokens' places hold the rest's gradient by now
+                if constexpr (TH <= 32) own.put_listed(te, w, g * in.c, c2, list, d);
             }
-            if (me == 0) te.loss[r] = Q != Q ? NAN : part;
-        }
-        if (kGrad && !none) {
-            group_sync<TH>();  // the listed tokens' places hold the rest's gradient by now
-            if (lister) {
-                const float gc = g * in.c, inv = reciprocal(all.s);
-                for (int e = me, i = 0; e < te.k; e += L, ++i)
-                    if ((first >> i) & 1u) {
-                        const int id = list[e].id;
-                        float w = list[e].q;
-                        if (twice) {
-                            w = 0.f;
-                            for (int l = 0; l < te.k; ++l)
-                                if (list[l].id == id) w += list[l].q;
-                        }
-                        const float pi = ex2(exponent(list[e].x, all.m, c2)) * inv;
-                        narrow(gc * (Q * pi - w), d + id);
-                    }
-            }
+        } else if (more) {
+            next.template rest<TH>(refilled, tid);
+            p = coming;
+            ie = first_lanes ? p.edge(tid) : -1;
+            edge = ie >= 0 ? widen(p.x[ie]) : -kInf;
         }
         if (!more) break;
     }
@@ -410,7 +527,7 @@ int distill(const void* logits, int dtype, int64_t S, int n, int V, int64_t stri
         return MIMI_RVQ_EINVAL;
     const Shape sh = shape_of(S * n, V, size, k <= kShortTop ? 16 : 0, true);
     const RowsIn in{logits, stride_s, stride_n, S * n, n, V, scale, sh.log_cluster,
-                    slots_of(V, size, sh.log_cluster) + k};
+                    slots_of(V, size, sh.log_cluster) + (k + 1) / 2};
     const TeacherIn te{ids, teacher, teacher_dtype == MIMI_RVQ_BF16, k, tail, g, loss, dlogits,
                        d_stride_s, d_stride_n, reinterpret_cast<unsigned long long*>(n_bad)};
     if (dtype == MIMI_RVQ_BF16)

@@ -261,9 +261,9 @@ __device__ __noinline__ int take_rounds(TopShared<TH>& sh, const Part<T> p, cons
         }
         if constexpr (TH > 32) {
             if ((tid & 31) == 0) sh.last[tid / 32] = best;
-            __syncthreads();
+            group_sync<TH>();
             for (int w = 0; w < TH / 32; ++w) best = sh.last[w] > best ? sh.last[w] : best;
-            __syncthreads();
+            group_sync<TH>();
         }
         if (best == 0) return q;
         if (tid == 0) put(q, best);
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
         const uint4* vectors = reinterpret_cast<const uint4*>(p.x + p.first);
         if constexpr (kTop) {
             if (tid < 32) find_bound(tops, tid, o.k);
-            __syncthreads();
+            group_sync<TH>();
             const float bound = tops.bound;
             if (__any_sync(kFull, top >= bound)) {
                 // the logits that reach it, from the chunks whose maximum does: each lane goes
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
                 }
                 if (ie >= 0) keep(edge, ie);
             }
-            __syncthreads();
+            group_sync<TH>();
             n = tops.count;
         }
         if (lc) {  // the first CTA gets the others' triples and keys
