@@ -112,6 +112,7 @@ struct TopShared {
 // The keys that a cluster's CTAs give its first one.
 struct TopLists {
     Key of[kMaxCluster][kMaxTop];
+    alignas(16) Key all[kMaxCluster * kMaxTop + 8];  // together
     int count[kMaxCluster];
 };
 
@@ -226,18 +227,22 @@ __device__ __forceinline__ int collect(TopShared<32>& sh, const Part<T>& p, cons
     return n;
 }
 
-// put(place, key) for the k largest of the list's n keys, and nothing for places past n; by G
-// threads together (a warp or the group).
-template <int G, int TH, typename Put>
-__device__ __forceinline__ void order_list(TopShared<TH>& sh, int n, int tid, int k, Put&& put) {
-    if (tid < 8) sh.list[n + tid] = 0;  // a round number to count
+// put(place, key) for the k largest of a list's n keys, and nothing for places past n; by G
+// threads together (a warp or the group). The list has room for 8 more.
+template <int G, typename Put>
+__device__ __forceinline__ void order_list(Key* list, int n, int tid, int k, Put&& put) {
+    if (tid < 8) list[n + tid] = 0;  // a round number to count
     group_sync<G>();
     for (int i = tid; i < n; i += G) {
-        const Key key = sh.list[i];
+        const Key key = list[i];
         int place = 0;
-        for (int l = 0; l < n; l += 8)
+        for (int l = 0; l < n; l += 8) {
+            ulonglong2 q[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) place += sh.list[l + q] > key;
+            for (int u = 0; u < 4; ++u) q[u] = *reinterpret_cast<const ulonglong2*>(list + l + 2 * u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) place += (q[u].x > key) + (q[u].y > key);
+        }
         if (place < k) put(place, key);
     }
 }
@@ -295,16 +300,15 @@ __device__ __forceinline__ void put_top(TopShared<TH>& sh, const ValuesOut& o, i
         for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
     } else if (tid < 32) {  // a CTA's other warps go on
         if (broken) n = 0;
-        else order_list<32>(sh, n, tid, o.k, out);
+        else order_list<32>(sh.list, n, tid, o.k, out);
         for (int i = n + tid; i < o.k; i += 32) out(i, Key(0));
     }
 }
 
 // The same from the lists that the cluster's CTAs gave.
 template <int TH>
-__device__ __forceinline__ void put_cluster_top(TopShared<TH>& sh, const TopLists& lists,
-                                                int cluster, const ValuesOut& o, int64_t r,
-                                                const Stats& st, float c, int tid) {
+__device__ __forceinline__ void put_cluster_top(TopLists& lists, int cluster, const ValuesOut& o,
+                                                int64_t r, const Stats& st, float c, int tid) {
     const bool broken = !(st.s < kInf);
     const float ln_s = ln(st.s), m = st.m;
     int32_t* const ids = o.top_ids == nullptr ? nullptr : o.top_ids + r * o.k;
@@ -315,23 +319,12 @@ __device__ __forceinline__ void put_cluster_top(TopShared<TH>& sh, const TopList
             lps[place] = broken ? NAN : key ? log_prob(key_value(key), c, m, ln_s) : -kInf;
     };
     int n = 0;
-    for (int l = 0; l < cluster && !broken; ++l) n += lists.count[l];
-    if (!broken)
-        for (int i = tid; i < n; i += TH) {
-            int l = 0, e = i;
-            while (e >= lists.count[l]) e -= lists.count[l++];
-            const Key key = lists.of[l][e];
-            int place = 0;
-            for (int l2 = 0; l2 < cluster; ++l2) {
-                const int m2 = lists.count[l2];
-                int e2 = 0;
-                for (; e2 + 4 <= m2; e2 += 4)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) place += lists.of[l2][e2 + q] > key;
-                for (; e2 < m2; ++e2) place += lists.of[l2][e2] > key;
-            }
-            if (place < o.k) out(place, key);
-        }
+    for (int l = 0; l < cluster && !broken; ++l) {
+        const int more = lists.count[l];
+        for (int e = tid; e < more; e += TH) lists.all[n + e] = lists.of[l][e];
+        n += more;
+    }
+    order_list<TH>(lists.all, n, tid, o.k, out);
     for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
 }
 
@@ -455,9 +448,9 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
         const int64_t r = row.r;
         const Part<T> p = part_at(row);
         const int chunks = chunks_of(p);
-        const int t = first_warp ? target_of(tk, token, in.V, tid == 0) : -1;
         const int ie = first_warp ? p.edge(tid) : -1;
         const float edge = ie < 0 ? -kInf : widen(p.x[ie]);
+        const int t = first_warp ? target_of(tk, token, in.V, tid == 0) : -1;
         const float xt = t >= 0 ? widen(p.x[t]) : 0.f;
         row.next(in.n);
         token = first_warp ? token_at(tk, row, in.rows) : -1;
@@ -604,7 +597,7 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
                 if (n > TopShared<TH>::kCap) {
                     n = take_rounds<TH>(tops, p, vectors, edge, tid, o.k, give);
                 } else if (n > o.k) {
-                    order_list<TH>(tops, n, tid, o.k, give);
+                    order_list<TH>(tops.list, n, tid, o.k, give);
                     n = o.k;
                 } else {
                     for (int i = tid; i < n; i += TH) give(i, tops.list[i]);
@@ -618,7 +611,7 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
             if (tid == 0) put_values(o, r, t, xt, in.c, st);
             if constexpr (kTop) {
                 const bool over = n > TopShared<TH>::kCap;
-                if (lc) put_cluster_top(tops, lists, cluster, o, r, st, in.c, tid);
+                if (lc) put_cluster_top<TH>(lists, cluster, o, r, st, in.c, tid);
                 else put_top<TH>(tops, o, r, n, over, st, in.c, tid, p, vectors, edge);
             }
         }
