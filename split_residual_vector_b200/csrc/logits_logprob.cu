@@ -14,9 +14,9 @@
 // is such a bound (k threads hold a logit that reaches it). One warp finds it by
 // bisecting the values' top 16 bits; only warps with a maximum that reaches it
 // look at their logits again and append those that do to a short list, which is
-// ordered by counting. The order of appending has no influence. A list that
-// overflows (rows of few distinct values) is replaced by k rounds that each
-// take the largest key below the last.
+// ordered by counting. The order of appending has no influence. Where the list
+// overflows (rows of few distinct values), the bound is bisected over the keys
+// themselves, which all differ, until between k and the list's length reach it.
 //
 // Gradient: d x_i = c p_i [(z - a) - b (ln p_i + H)] + c a [i = token] from the
 // row in shared memory, so that it is read once from global memory and written
@@ -96,18 +96,20 @@ __device__ __forceinline__ void put_values(const ValuesOut& o, int64_t r, int t,
 
 // ------------------------------------------------------------------ alternatives
 
-// Alternatives a warp's row may have: 32 maxima bound the list's length by about
-// -32 ln(1 - k / 32) logits on rows in random order, 44 at k = 24.
-constexpr int kWarpTop = 24;
+// g maxima bound the list's length by about -g ln(1 - k / g) logits on rows in random order. So
+// lists of up to kFewTop take 32 maxima (44 logits at k = 24), up to kWarpTop 128 (89 at k = 64),
+// longer ones 256 (177 at k = 128).
+constexpr int kFewTop = 24, kWarpTop = 64;
 
 template <int TH>
 struct TopShared {
-    static constexpr int kCap = TH == 32 ? 128 : 256;
-    alignas(16) uint32_t most[TH == 32 ? 4 : TH];  // the threads' maxima
+    static constexpr int kCap = TH == 32 ? 256 : 512;
+    uint32_t most[2][TH == 32 ? 1 : TH];  // the threads' maxima of two halves of their logits
     float bound;
     int count;
     alignas(16) Key list[kCap + 8];
     Key last[TH == 32 ? kCap / 4 : TH / 32];  // a warp: the vectors that have a listed logit
+    int counts[2][TH / 32];
 };
 // The keys that a cluster's CTAs give its first one.
 struct TopLists {
@@ -116,11 +118,11 @@ struct TopLists {
     int count[kMaxCluster];
 };
 
-// f(value, id) for this thread's logits of the share.
+// f(value, id) for this thread's logits of the share, which are in `buf` (any memory).
 template <int TH, typename T, typename F>
 __device__ __forceinline__ void each_logit(const uint4* buf, const Part<T>& p, int tid, float edge,
                                            F&& f) {
-#pragma unroll 1
+#pragma unroll 2
     for (int i = tid; i < p.nv; i += TH) {
         const uint4 q = buf[i];
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -161,34 +163,99 @@ __device__ __forceinline__ float bound_of(const uint32_t (&q)[kN], int k) {
 }
 
 // Leaves a CTA's bound for its k largest logits in sh.bound; called by its first warp when the
-// threads' maxima are there. Lists of up to 24 take the maxima of 4 threads as one value.
+// threads' maxima are there; short lists take the maxima of 4 threads as one value.
 template <int TH>
 __device__ __forceinline__ void find_bound(TopShared<TH>& sh, int tid, int k) {
-    static_assert(TH == 128, "four maxima a lane");
-    const uint4 v = *reinterpret_cast<const uint4*>(&sh.most[4 * tid]);
-    float bound;
-    if (k <= kWarpTop) {
-        const uint32_t q[1] = {max(max(v.x, v.y), max(v.z, v.w))};
-        bound = bound_of(q, k);
-    } else {
-        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-        bound = bound_of(q, k);
-    }
+    static_assert(TH == 128, "eight maxima a lane");
+    uint32_t q[8], half[4], all[1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = sh.most[i / 4][tid + 32 * (i % 4)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) half[i] = max(q[i], q[i + 4]);
+    all[0] = max(max(half[0], half[1]), max(half[2], half[3]));
+    const float bound = k <= kFewTop ? bound_of(all, k) : k <= kWarpTop ? bound_of(half, k) : bound_of(q, k);
     if (tid == 0) {
         sh.bound = bound;
         sh.count = 0;
     }
 }
 
+// The list of a share whose logits above sh's bound were more than it holds: bisects a bound over
+// their keys; returns the number of keys, between min(k, logits above -inf) and kCap.
+template <int TH, typename T>
+__device__ __noinline__ int refine(TopShared<TH>& sh, const Part<T> p, const uint4* buf, float edge,
+                                   float bound, int tid, int k) {
+    constexpr int kCap = TopShared<TH>::kCap, kWarps = TH / 32;
+    Key top = 0;
+    each_logit<TH>(buf, p, tid, edge, [&](float x, int id) {
+        const Key key = key_of(x, id);
+        if (x >= bound && key > top) top = key;
+    });
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const Key other = __shfl_xor_sync(kFull, top, o);
+        top = other > top ? other : top;
+    }
+    if constexpr (TH > 32) {
+        if ((tid & 31) == 0) sh.last[tid / 32] = top;
+        group_sync<TH>();
+        for (int w = 0; w < kWarps; ++w) top = sh.last[w] > top ? sh.last[w] : top;
+    }
+    // more than kCap keys are at least lo, none is above hi
+    Key lo = (Key)order_of(bound) << 32, hi = top, at = lo;
+    for (int parity = 0;; parity ^= 1) {
+        at = lo + (hi - lo + 1) / 2;
+        unsigned n = 0;
+        each_logit<TH>(buf, p, tid, edge, [&](float x, int id) { n += x >= bound && key_of(x, id) >= at; });
+        n = __reduce_add_sync(kFull, n);
+        if constexpr (TH > 32) {
+            if ((tid & 31) == 0) sh.counts[parity][tid / 32] = (int)n;
+            group_sync<TH>();
+            n = 0;
+            for (int w = 0; w < kWarps; ++w) n += sh.counts[parity][w];
+        }
+        if ((int)n > kCap) lo = at;
+        else if ((int)n < k) hi = at - 1;
+        else break;
+        if (lo >= hi) break;  // cannot be: keys differ, so some bound has between k and kCap
+    }
+    if (tid == 0) sh.count = 0;
+    group_sync<TH>();
+    each_logit<TH>(buf, p, tid, edge, [&](float x, int id) {
+        const Key key = key_of(x, id);
+        if (x >= bound && key >= at) {
+            const int place = atomicAdd(&sh.count, 1);
+            if (place < kCap) sh.list[place] = key;
+        }
+    });
+    group_sync<TH>();
+    return min(sh.count, kCap);
+}
+
 // A warp's row: the logits that reach the bound, as unordered keys in sh.list; returns their
-// number, at least min(k, the logits above -inf); past kCap the list is not complete. Vectors
-// with such a logit are listed first, then their elements are spread over the lanes.
+// number, at least min(k, the logits above -inf). Vectors with such a logit are listed first, then
+// their elements are spread over the lanes.
 template <typename T>
 __device__ __forceinline__ int collect(TopShared<32>& sh, const Part<T>& p, const uint4* buf,
                                        float edge, float top, int lane, int k) {
     constexpr int kCap = TopShared<32>::kCap, kPer = Elem<T>::kPer;
-    const uint32_t q[1] = {order_of(top)};
-    const float bound = bound_of(q, k);
+    float bound;
+    if (k <= kFewTop) {
+        const uint32_t q[1] = {order_of(top)};
+        bound = bound_of(q, k);
+    } else {  // a lane's vectors in four parts
+        float m[4] = {edge, -kInf, -kInf, -kInf};
+        for (int base = lane; base < p.nv; base += 128)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (base + 32 * u < p.nv) {
+                    const uint4 v = buf[base + 32 * u];
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    m[u] = fmaxf(m[u], vector_max<T>(w));
+                }
+        const uint32_t q[4] = {order_of(m[0]), order_of(m[1]), order_of(m[2]), order_of(m[3])};
+        bound = bound_of(q, k);
+    }
     const unsigned below = (1u << lane) - 1u;
     uint16_t* vectors = reinterpret_cast<uint16_t*>(sh.last);  // kCap of them
     int nv = 0;
@@ -204,7 +271,7 @@ __device__ __forceinline__ int collect(TopShared<32>& sh, const Part<T>& p, cons
         if (hit && nv + __popc(hits & below) < kCap) vectors[nv + __popc(hits & below)] = (uint16_t)i;
         nv += __popc(hits);
     }
-    if (nv > kCap) return kCap + 1;
+    if (nv > kCap) return refine<32>(sh, p, buf, edge, bound, lane, k);
     __syncwarp();
     int n = 0;
     auto keep = [&](float x, int id, bool any) {
@@ -224,7 +291,7 @@ __device__ __forceinline__ int collect(TopShared<32>& sh, const Part<T>& p, cons
     const int ie = p.edge(lane);
     keep(edge, ie, ie >= 0);
     __syncwarp();
-    return n;
+    return n > kCap ? refine<32>(sh, p, buf, edge, bound, lane, k) : n;
 }
 
 // put(place, key) for the k largest of a list's n keys, and nothing for places past n; by G
@@ -247,68 +314,12 @@ __device__ __forceinline__ void order_list(Key* list, int n, int tid, int k, Put
     }
 }
 
-// The k largest of the share without a list: k rounds that each find the largest key below the
-// last one; returns how many there are (one thread puts them).
-template <int TH, typename T, typename Put>
-__device__ __noinline__ int take_rounds(TopShared<TH>& sh, const Part<T> p, const uint4* buf,
-                                        float edge, int tid, int k, Put put) {
-    Key last = ~Key(0);
-    for (int q = 0; q < k; ++q) {
-        Key best = 0;
-        each_logit<TH>(buf, p, tid, edge, [&](float x, int id) {
-            const Key key = key_of(x, id);
-            if (x > -kInf && key < last && key > best) best = key;
-        });
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const Key other = __shfl_xor_sync(kFull, best, o);
-            best = other > best ? other : best;
-        }
-        if constexpr (TH > 32) {
-            if ((tid & 31) == 0) sh.last[tid / 32] = best;
-            group_sync<TH>();
-            for (int w = 0; w < TH / 32; ++w) best = sh.last[w] > best ? sh.last[w] : best;
-            group_sync<TH>();
-        }
-        if (best == 0) return q;
-        if (tid == 0) put(q, best);
-        last = best;
-    }
-    return k;
-}
-
 // ------------------------------------------------------------------ forward
 
-// A row's alternatives from the n keys of sh.list, or (over: the list is not complete) by rounds
-// over the logits in `buf`.
-template <int TH, typename T>
-__device__ __forceinline__ void put_top(TopShared<TH>& sh, const ValuesOut& o, int64_t r, int n,
-                                        bool over, const Stats& st, float c, int tid,
-                                        const Part<T>& p, const uint4* buf, float edge) {
-    const bool broken = !(st.s < kInf);
-    const float ln_s = ln(st.s);
-    int32_t* const ids = o.top_ids == nullptr ? nullptr : o.top_ids + r * o.k;
-    float* const lps = o.top_logprob == nullptr ? nullptr : o.top_logprob + r * o.k;
-    const float m = st.m;
-    auto out = [=](int place, Key key) {
-        if (ids != nullptr) ids[place] = key ? key_id(key) : -1;
-        if (lps != nullptr)
-            lps[place] = broken ? NAN : key ? log_prob(key_value(key), c, m, ln_s) : -kInf;
-    };
-    if (over && !broken) {
-        n = take_rounds<TH>(sh, p, buf, edge, tid, o.k, out);
-        for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
-    } else if (tid < 32) {  // a CTA's other warps go on
-        if (broken) n = 0;
-        else order_list<32>(sh.list, n, tid, o.k, out);
-        for (int i = n + tid; i < o.k; i += 32) out(i, Key(0));
-    }
-}
-
-// The same from the lists that the cluster's CTAs gave.
-template <int TH>
-__device__ __forceinline__ void put_cluster_top(TopLists& lists, int cluster, const ValuesOut& o,
-                                                int64_t r, const Stats& st, float c, int tid) {
+// A row's alternatives from the n keys of a list, by G threads.
+template <int G>
+__device__ __forceinline__ void put_top(Key* list, const ValuesOut& o, int64_t r, int n,
+                                        const Stats& st, float c, int tid) {
     const bool broken = !(st.s < kInf);
     const float ln_s = ln(st.s), m = st.m;
     int32_t* const ids = o.top_ids == nullptr ? nullptr : o.top_ids + r * o.k;
@@ -318,14 +329,9 @@ __device__ __forceinline__ void put_cluster_top(TopLists& lists, int cluster, co
         if (lps != nullptr)
             lps[place] = broken ? NAN : key ? log_prob(key_value(key), c, m, ln_s) : -kInf;
     };
-    int n = 0;
-    for (int l = 0; l < cluster && !broken; ++l) {
-        const int more = lists.count[l];
-        for (int e = tid; e < more; e += TH) lists.all[n + e] = lists.of[l][e];
-        n += more;
-    }
-    order_list<TH>(lists.all, n, tid, o.k, out);
-    for (int i = n + tid; i < o.k; i += TH) out(i, Key(0));
+    if (broken) n = 0;
+    else order_list<G>(list, n, tid, o.k, out);
+    for (int i = n + tid; i < o.k; i += G) out(i, Key(0));
 }
 
 // Rows of up to 8 KB, each in its group's shared memory: half a warp a row, or a warp where
@@ -374,13 +380,9 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
         if constexpr (kTop) {
             st = join_group<TH, true>(joint[group], st, tid, 0, c2);
             const int n = collect(tops[group], p, buf, edge, top, tid, o.k);
-            const bool over = n > TopShared<32>::kCap;
             if (tid == 0) put_values(o, r, t, xt, in.c, st);
-            const Part<T> here = p;
-            const float here_edge = edge;
-            if (!over) send_next();
-            put_top<TH>(tops[group], o, r, n, over, st, in.c, tid, here, buf, here_edge);
-            if (over) send_next();
+            send_next();
+            put_top<TH>(tops[group].list, o, r, n, st, in.c, tid);
         } else {
             send_next();
             st = join_group<TH, true>(joint[group], st, tid, 0, c2);
@@ -454,7 +456,8 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
         const float xt = t >= 0 ? widen(p.x[t]) : 0.f;
         row.next(in.n);
         token = first_warp ? token_at(tk, row, in.rows) : -1;
-        float top = -kInf, m = -kInf;  // the thread's maximum, the warp's
+        float m = -kInf;  // the warp's maximum
+        float halves_top[2] = {edge, -kInf};  // the thread's, of two halves of its logits
         Scale k(c2, m);
         Pair s2 = 0, w2 = 0;  // (0, 0)
         for (int c = 0; c < chunks; ++c) {
@@ -480,14 +483,22 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
             }
             float mx;
             if constexpr (sizeof(T) == 4) {
-                mx = vector_max<T>(w[0]);
+                float a = -kInf, b = -kInf;
 #pragma unroll
-                for (int u = 1; u < kU; ++u) mx = fmaxf(mx, vector_max<T>(w[u]));
+                for (int u = 0; u < kU; ++u) {
+                    a = fmaxf(a, fmaxf(__uint_as_float(w[u][0]), __uint_as_float(w[u][1])));
+                    b = fmaxf(b, fmaxf(__uint_as_float(w[u][2]), __uint_as_float(w[u][3])));
+                }
+                halves_top[0] = fmaxf(halves_top[0], a);
+                halves_top[1] = fmaxf(halves_top[1], b);
+                mx = fmaxf(a, b);
             } else {
                 uint32_t a = Elem<T>::kFill;
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
                     a = max_bf16x2(a, max_bf16x2(max_bf16x2(w[u][0], w[u][1]), max_bf16x2(w[u][2], w[u][3])));
+                halves_top[0] = fmaxf(halves_top[0], bf16_lo_to_f32(a));
+                halves_top[1] = fmaxf(halves_top[1], bf16_hi_to_f32(a));
                 mx = fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a));
             }
             if constexpr (kTop) {
@@ -495,7 +506,6 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
                 of = c < kRemember ? mx : fmaxf(of, mx);
             }
             if (c == chunks - 1) mx = fmaxf(mx, edge);
-            top = fmaxf(top, mx);
             if (__any_sync(kFull, mx > m)) {  // a new maximum: the sums so far move to it
                 const float m_new = fmaxf(m, lanes_max<32>(mx));
                 const Scale k_new(c2, m_new);
@@ -547,7 +557,11 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
             st.s = fmaf(s, back, e);
             st.w = fmaf(fmaf(-k.shift, s, w0 + w1), back, e * te);
         }
-        if constexpr (kTop) tops.most[tid] = order_of(top);
+        const float top = fmaxf(halves_top[0], halves_top[1]);
+        if constexpr (kTop) {
+            tops.most[0][tid] = order_of(halves_top[0]);
+            tops.most[1][tid] = order_of(halves_top[1]);
+        }
         st = join_group<TH, true>(joint, st, tid, parity, c2);
         int n = 0;
         const uint4* vectors = reinterpret_cast<const uint4*>(p.x + p.first);
@@ -586,6 +600,7 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
             }
             group_sync<TH>();
             n = tops.count;
+            if (n > TopShared<TH>::kCap) n = refine<TH>(tops, p, vectors, edge, bound, tid, o.k);
         }
         if (lc) {  // the first CTA gets the others' triples and keys
             if (!started) cluster_wait();
@@ -594,9 +609,7 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
             if constexpr (kTop) {
                 const uint32_t to = cluster_map(smem_u32(&lists.of[rank][0]), 0);
                 auto give = [to](int place, Key key) { st_cluster_u64(to + 8 * place, key); };
-                if (n > TopShared<TH>::kCap) {
-                    n = take_rounds<TH>(tops, p, vectors, edge, tid, o.k, give);
-                } else if (n > o.k) {
+                if (n > o.k) {
                     order_list<TH>(tops.list, n, tid, o.k, give);
                     n = o.k;
                 } else {
@@ -610,9 +623,17 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
         if (rank == 0) {
             if (tid == 0) put_values(o, r, t, xt, in.c, st);
             if constexpr (kTop) {
-                const bool over = n > TopShared<TH>::kCap;
-                if (lc) put_cluster_top<TH>(lists, cluster, o, r, st, in.c, tid);
-                else put_top<TH>(tops, o, r, n, over, st, in.c, tid, p, vectors, edge);
+                if (lc) {
+                    n = 0;
+                    for (int l = 0; l < cluster; ++l) {
+                        const int more = lists.count[l];
+                        for (int e = tid; e < more; e += TH) lists.all[n + e] = lists.of[l][e];
+                        n += more;
+                    }
+                    put_top<TH>(lists.all, o, r, n, st, in.c, tid);
+                } else if (tid < 32) {  // the other warps go on
+                    put_top<32>(tops.list, o, r, n, st, in.c, tid);
+                }
             }
         }
         if (lc && row.r < in.rows) cluster_sync();  // the first CTA has read what it was given
@@ -737,10 +758,10 @@ cudaError_t forward_of(int threads, const RowsIn& in, const TokensIn& tk, const 
                        cudaStream_t s) {
     constexpr int kShort = kTop ? 32 : 16;
     if (threads == kShort)  // the last figures: static shared memory, rounded up
-        return launch_rows<&k_logprob<T, kShort, kTop>, kShort, 0>(in, kTop ? 6 * 1024 : 512, s, in, tk, o);
+        return launch_rows<&k_logprob<T, kShort, kTop>, kShort, 0>(in, kTop ? 12 * 1024 : 512, s, in, tk, o);
     RowsIn with_ring = in;
     with_ring.slots = kStages * kChunk + (kTop && in.log_cluster ? (int)sizeof(TopLists) / 16 + 1 : 0);
-    return launch_rows<&k_logprob_long<T, kTop>, kLong, 0>(with_ring, kTop ? 8 * 1024 : 1024, s, with_ring, tk, o);
+    return launch_rows<&k_logprob_long<T, kTop>, kLong, 0>(with_ring, kTop ? 11 * 1024 : 1024, s, with_ring, tk, o);
 }
 
 template <typename T>
