@@ -415,6 +415,7 @@ def _logit_rows(logits):
     assert logits.is_cuda and logits.dim() in (2, 3), "logits are [S, V] or [S, n, V] on CUDA"
     shape, stride = logits.shape, logits.stride()
     assert shape[-1] <= 1 or stride[-1] == 1, "a row's logits are contiguous"
+    assert shape[-1] <= MAX_VOCAB, f"rows have at most {MAX_VOCAB} logits"
     if logits.dim() == 2:
         return shape[:1], _dtype_flag(logits), shape[0], 1, shape[1], stride[0], 0
     return shape[:2], _dtype_flag(logits), shape[0], shape[1], shape[2], stride[0], stride[1]

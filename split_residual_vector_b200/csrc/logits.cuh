@@ -212,7 +212,8 @@ __device__ __forceinline__ float exponent(float x, float m, float c2) {
     return max_nan((x - (m == -kInf ? 0.f : m)) * c2, kLow);
 }
 
-// ln of a sum (0: -inf); the approximate logarithm is within 2^-22.
+// ln of a sum (0: -inf) for gradients, within 2^-22 absolutely near 1; values take logf, as the
+// logarithm of a token that is nearly certain is its log probability.
 __device__ __forceinline__ float ln(float s) {
     float r;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
@@ -609,7 +610,7 @@ inline bool rows_ok(int dtype, int64_t S, int n, int V, int64_t ss, int64_t sn, 
     if (S < 0 || n < 0 || n > 65536 || S > (int64_t(1) << 40)) return false;
     if (V < 1 || V > MIMI_RVQ_MAX_VOCAB || ss < 0 || sn < 0) return false;
     if ((__int128)ss * S + (__int128)sn * n > ((__int128)1 << 58)) return false;  // no offset wraps
-    return scale > 0.f && scale < kInf;
+    return scale > 0.f && scale <= 1.0e30f;
 }
 
 // Rows of a gradient must not share memory: the smaller stride holds a row, the larger one all

@@ -231,7 +231,7 @@ struct Lister {
     }
     __device__ __forceinline__ void put_loss(const TeacherIn& te, int64_t r, int me, const Whole& w,
                                              float c) const {
-        const float ln_s = ln(w.all.s);
+        const float ln_s = logf(w.all.s);
         float part = 0.f;
         if (!w.empty) {
             each(te.k, [&](int i) {
@@ -240,7 +240,7 @@ struct Lister {
             });
             part = lanes_sum<TH>(part);
             if (w.qr > 0.f)
-                part += w.qr * (logf(w.qr) - (c * (w.rest.m - w.all.m) + ln(w.rest.s) - ln_s));
+                part += w.qr * (logf(w.qr) - (c * (w.rest.m - w.all.m) + logf(w.rest.s) - ln_s));
         }
         if (me == 0) te.loss[r] = w.Q != w.Q ? NAN : part;
     }

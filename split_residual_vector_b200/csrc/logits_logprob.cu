@@ -86,7 +86,7 @@ __device__ __forceinline__ int target_of(const TokensIn& tk, int32_t t, int V, b
 
 __device__ __forceinline__ void put_values(const ValuesOut& o, int64_t r, int t, float xt, float c,
                                            const Stats& st) {
-    const float ln_s = ln(st.s);
+    const float ln_s = logf(st.s);
     const bool none = st.s == 0.f;
     if (o.logprob != nullptr)
         o.logprob[r] = t < 0 ? 0.f : none ? -kInf : log_prob(xt, c, st.m, ln_s);
@@ -321,7 +321,7 @@ template <int G>
 __device__ __forceinline__ void put_top(Key* list, const ValuesOut& o, int64_t r, int n,
                                         const Stats& st, float c, int tid) {
     const bool broken = !(st.s < kInf);
-    const float ln_s = ln(st.s), m = st.m;
+    const float ln_s = logf(st.s), m = st.m;
     int32_t* const ids = o.top_ids == nullptr ? nullptr : o.top_ids + r * o.k;
     float* const lps = o.top_logprob == nullptr ? nullptr : o.top_logprob + r * o.k;
     auto out = [=](int place, Key key) {

@@ -76,7 +76,7 @@ def logprob(x, tokens, pad=-1, c=1.0):
         there, at = targets(tokens.reshape(r.none.shape), r.x.shape[-1], pad)
         lp, t = r.logp.gather(-1, at).squeeze(-1), r.t_logp.gather(-1, at).squeeze(-1)
         lp = torch.where(r.none, -math.inf, lp)
-        out["logprob"] = (torch.where(there, lp, 0.0), t)
+        out["logprob"] = (torch.where(there, lp, 0.0), torch.where(there, t, 0.0))
     return out
 
 

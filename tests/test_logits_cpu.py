@@ -62,7 +62,7 @@ def test_sizes_are_checked_before_anything_else(lib, call):
     assert call(lib, V=3 << 17, ss=3 << 17) == OK
     for over in BAD_ROWS:
         assert call(lib, **over) == EINVAL, over
-    for scale in (0.0, -1.0, math.inf, math.nan):
+    for scale in (0.0, -1.0, 1e31, math.inf, math.nan):
         assert call(lib, scale=scale) == EINVAL
 
 

@@ -107,6 +107,57 @@ def test_top_alternatives_with_ties(S, V, k, dtype):
     near(r.top_logprob, lp, t)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [130, 311, 600, 811, 2048, 2051, 4100, 32001])
+def test_top_alternatives_of_ordinary_rows(V, dtype):
+    """Every way the list's bound is found: from 32, 128 and 256 maxima, too few of them, and
+    (sorted rows: one thread has all the largest) far too many logits above it."""
+    x = make(6, 0, V, dtype, seed=V)
+    x[1] = torch.sort(x[1].float(), descending=True).values.to(dtype)
+    x[2] = torch.sort(x[2].float()).values.to(dtype)
+    for k in (24, 25, 64, 65, 100, 128):
+        r = pkg().token_logprobs(x, top_k=k)
+        ids, lp, t = ref.top(x, k)
+        assert torch.equal(r.top_ids.long(), ids[:, 0]), k
+        near(r.top_logprob, lp, t, f"k {k}")
+
+
+@pytest.mark.parametrize("S,n,V,dtype", [(9001, 3, 65, BF16), (3000, 7, 130, F32), (2500, 0, 4104, BF16),
+                                         (2500, 0, 4104, F32), (1500, 0, 17001, BF16), (700, 0, 20001, F32),
+                                         (130, 0, 70001, F32), (90, 0, 150001, BF16)])
+def test_many_rows(S, n, V, dtype):
+    """More rows than are resident at once, so that every group walks several; among them rows
+    without target, list or upstream gradient, and rows of NaN in their places."""
+    p = pkg()
+    x = make(S, n, V, dtype, seed=30)
+    lead = x.shape[:-1]
+    g = gen(31)
+    off = torch.rand(lead, device="cuda", generator=g) < 0.3
+    x[off & (torch.rand(lead, device="cuda", generator=g) < 0.2)] = math.nan
+    tok = torch.where(off, V, tokens_for(S, n, V))
+    r = p.token_logprobs(x, tok, pad=V, top_k=9)
+    check_values(r, x, tok, V, k=9)
+    check_values(p.token_logprobs(x, tok, pad=V), x, tok, V)
+    a, b = torch.randn((2, *lead), device="cuda", generator=g)
+    b[off] = 0
+    b[torch.rand(lead, device="cuda", generator=g) < 0.5] = 0
+    near(p.token_logprobs_grad(x, tok, a, b, pad=V), *ref.logprob_grad(x, tok, a, b, None, V))
+    d, v = p.token_logprobs_grad(x, tok, a, pad=V, values=True)
+    near(d, *ref.logprob_grad(x, tok, a, pad=V))
+    check_values(v, x, tok, V)
+    ids = torch.randint(0, V, (*lead, 21), device="cuda", generator=g, dtype=torch.int32)
+    ids[off] = -1
+    t = torch.log_softmax(torch.randn(ids.shape, device="cuda", generator=g), -1) - 0.2
+    a[torch.rand(lead, device="cuda", generator=g) < 0.3] = 0
+    for tail in (False, True):
+        loss, t_loss, d, t_d = ref.distill(x, ids, t, a, tail)
+        near(p.distill_topk(x, ids, t, tail=tail), loss, t_loss, "loss")
+        near(p.distill_topk_grad(x, ids, t, a, tail=tail), d, t_d, "dlogits")
+        got, l2 = p.distill_topk_grad(x, ids, t, a, tail=tail, loss=True)
+        near(l2, loss, t_loss, "loss with gradient")
+        near(got, d, t_d, "dlogits with loss")
+
+
 def special_rows(V, dtype):
     """Rows on which a softmax can go wrong; NaN only in the rows from 7 on."""
     x = make(12, 0, V, dtype, seed=5)
@@ -412,7 +463,7 @@ def test_argument_errors():
     x = make(4, 2, 64, F32)
     tok = tokens_for(4, 2, 64)
     ids, t = teacher_for(x, 3, False)
-    for bad in (0.0, -1.0, math.inf, math.nan):
+    for bad in (0.0, -1.0, 1e31, math.inf, math.nan):
         with pytest.raises(p.MimiRVQError):
             p.token_logprobs(x, tok, scale=bad)
     with pytest.raises(p.MimiRVQError):
