@@ -117,9 +117,9 @@ struct Lister {
                                          Entry* list) {
         const unsigned mask = lane_mask<TH>();
         int n = 0, bad = 0;
-        mine = first = 0;
+        mine = 0;
         tmax = -kInf;
-        broken = twice = false;
+        broken = false;
         __syncwarp(mask);  // the last row's list has been read
         each(te.k, [&](int i) {
             const int e = me + L * i, given = next_id[i];
@@ -133,20 +133,8 @@ struct Lister {
             tmax = fmaxf(tmax, lq[i]);
             broken |= !(lq[i] < kInf);
             if (e < te.k) list[e] = Entry{id[i], lq[i]};
-            const unsigned same = __match_any_sync(mask, id[i]);
-            bool again = (same & ((1u << (threadIdx.x & 31)) - 1u)) != 0;
-            if (i) {
-                __syncwarp(mask);
-                for (int l = 0; l < i * L; ++l) again |= list[l].id == id[i];
-            }
-            again &= there;
-            twice |= again;
-            if (there && (p.place(id[i]) >= 0 || (rank == 0 && p.in_edges(id[i])))) {
-                mine |= 1u << i;
-                if (!again) first |= 1u << i;
-            }
+            if (there && (p.place(id[i]) >= 0 || (rank == 0 && p.in_edges(id[i])))) mine |= 1u << i;
         });
-        twice = __any_sync(mask, twice);
         if (bad && rank == 0 && te.n_bad != nullptr)
             atomicAdd(te.n_bad, (unsigned long long)bad);
         tmax = lanes_max<TH>(tmax);
@@ -156,29 +144,39 @@ struct Lister {
     __device__ __forceinline__ bool empty(const TeacherIn& te) const {
         return !some || (!te.tail && tmax == -kInf && !broken);
     }
-    // reads the listed elements of this share and hides them
+    // Reads the listed elements of this share and hides them. In between the places' numbers stand
+    // there, which shows an id that is listed twice (a warp's match instruction on the ids before
+    // the row is here takes 600 cycles for each 32: 100 rows of 131072 with 128 entries 34 us, so 30).
     __device__ __forceinline__ void hide(const TeacherIn& te, const Part<T>& p, uint4* buf, T* edge,
-                                         bool others) {
-        auto cell = [&](int i) {
-            const int at = p.place(id[i]);
-            return at >= 0 ? reinterpret_cast<B*>(buf) + at
-                           : reinterpret_cast<B*>(edge) + p.edge_lane(id[i]);
-        };
-        each(te.k, [&](int i) {
-            if ((mine >> i) & 1u) {
-                B* at = cell(i);
-                x[i] = widen(*reinterpret_cast<const T*>(at));
-                if (!twice) *at = (B)Elem<T>::kFill;
-            } else if (others && id[i] >= 0) {
-                x[i] = widen(p.x[id[i]]);  // another CTA's; for the loss
-            }
-        });
-        if (twice) {
-            __syncwarp(lane_mask<TH>());
+                                         bool others, int me, const Entry* list) {
+        const unsigned mask = lane_mask<TH>();
+        auto each_mine = [&](auto&& f) {
             each(te.k, [&](int i) {
-                if ((mine >> i) & 1u) *cell(i) = (B)Elem<T>::kFill;
+                if (!((mine >> i) & 1u)) return;
+                const int at = p.place(id[i]);
+                f(i, at >= 0 ? reinterpret_cast<B*>(buf) + at
+                             : reinterpret_cast<B*>(edge) + p.edge_lane(id[i]));
             });
-        }
+        };
+        each_mine([&](int i, B* at) { x[i] = widen(*reinterpret_cast<const T*>(at)); });
+        __syncwarp(mask);
+        each_mine([&](int i, B* at) { *at = (B)(me + L * i); });
+        __syncwarp(mask);
+        bool lost = false;
+        each_mine([&](int i, B* at) { lost |= *at != (B)(me + L * i); });
+        twice = __any_sync(mask, lost);
+        each_mine([&](int, B* at) { *at = (B)Elem<T>::kFill; });
+        first = mine;
+        if (twice)  // the first of equal ids stands for all (places in the share are below k)
+            each(te.k, [&](int i) {
+                if (!((mine >> i) & 1u)) return;
+                for (int l = 0; l < me + L * i; ++l)
+                    if (list[l].id == id[i]) first &= ~(1u << i);
+            });
+        if (others)  // other CTAs' elements, for the loss
+            each(te.k, [&](int i) {
+                if (!((mine >> i) & 1u) && id[i] >= 0) x[i] = widen(p.x[id[i]]);
+            });
     }
     // the weights, and this share's listed logits, for the group
     __device__ __forceinline__ void weigh(const TeacherIn& te, int me, Entry* list,
@@ -385,7 +383,7 @@ __global__ void __launch_bounds__(block_of<TH>() + lister_of<TH>(), distill_bloc
             Whole w = nothing;
             if (!skipped(g)) {
                 group_sync<N>();  // the row is here
-                lister.hide(te, p, buf, ls.edge, lc != 0 && rank == 0);
+                lister.hide(te, p, buf, ls.edge, lc != 0 && rank == 0, me, list);
                 const bool empty = lister.empty(te);
                 if (me == 0) ls.empty = empty;
                 group_sync<N>();  // the listed tokens are hidden
@@ -451,7 +449,7 @@ __global__ void __launch_bounds__(block_of<TH>() + lister_of<TH>(), distill_bloc
             group_sync<N>();  // the row is here
             bool empty;
             if constexpr (TH <= 32) {
-                own.hide(te, p, buf, ls.edge, false);
+                own.hide(te, p, buf, ls.edge, false, tid, list);
                 empty = own.empty(te);
                 group_sync<N>();
             } else {
