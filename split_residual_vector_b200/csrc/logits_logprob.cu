@@ -424,19 +424,28 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
     auto part_at = [&](const RowWalk& w) {
         return Part<T>(static_cast<const T*>(in.x) + w.s * in.ss + w.j * in.sn, in.V, rank, lc);
     };
-    auto chunks_of = [](const Part<T>& p) { return max(1, (p.nv + kChunk - 1) / kChunk); };
+    // chunks begin on 128-byte lines: the first one's first `skip` places stay empty (rows of odd
+    // lengths would touch five lines with each warp's copy instead of four: 3750 x 32001 float32 93
+    // us, so 87; with alternatives it gains nothing, 103 against 108)
+    auto skip_of = [](const Part<T>& p) {
+        return kTop ? 0 : (int)((reinterpret_cast<uintptr_t>(p.x + p.first) >> 4) & 7u);
+    };
+    auto chunks_of = [&](const Part<T>& p) {
+        return max(1, (p.nv + skip_of(p) + kChunk - 1) / kChunk);
+    };
     // copies, ahead of the chunk that is read; one group of copies per call
     RowWalk ahead = row;
     Part<T> to_come = part_at(ahead);
     int next_chunk = 0, left_to_come = chunks_of(to_come), stage_in = 0, stage_out = 0;
     auto send = [&]() {
         if (ahead.r < in.rows) {
-            const int base = next_chunk * kChunk + tid;
-            const T* src = to_come.x + to_come.first + (size_t)base * kPer;
+            const int base = next_chunk * kChunk + tid - skip_of(to_come);
+            const T* src = to_come.x + to_come.first + (int64_t)base * kPer;
             uint4* dst = ring + stage_in * kChunk + tid;
 #pragma unroll
             for (int u = 0; u < kU; ++u)
-                if (base + u * TH < to_come.nv) copy16(dst + u * TH, src + (size_t)u * TH * kPer);
+                if (base + u * TH < to_come.nv && (u > 0 || base >= 0))
+                    copy16(dst + u * TH, src + (size_t)u * TH * kPer);
             ++next_chunk;
             if (--left_to_come == 0) {
                 ahead.next(in.n);
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
     for (int parity = 0; row.r < in.rows; parity ^= 1) {
         const int64_t r = row.r;
         const Part<T> p = part_at(row);
-        const int chunks = chunks_of(p);
+        const int chunks = chunks_of(p), skip = skip_of(p);
         const int ie = first_warp ? p.edge(tid) : -1;
         const float edge = ie < 0 ? -kInf : widen(p.x[ie]);
         const int t = first_warp ? target_of(tk, token, in.V, tid == 0) : -1;
@@ -472,9 +481,9 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             const uint4* at = ring + stage_out * kChunk + tid;
             stage_out = stage_out == kStages - 1 ? 0 : stage_out + 1;
-            const int left = p.nv - c * kChunk;
+            const int left = p.nv + skip - c * kChunk;
             uint32_t w[kU][4];
-            if (left >= kChunk) {
+            if (left >= kChunk && (c > 0 || skip == 0)) {
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
                     const uint4 q = at[u * TH];
@@ -484,7 +493,7 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
                     uint4 q = make_uint4(Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill);
-                    if (u * TH + tid < left) q = at[u * TH];
+                    if (u * TH + tid < left && (u > 0 || c > 0 || tid >= skip)) q = at[u * TH];
                     w[u][0] = q.x, w[u][1] = q.y, w[u][2] = q.z, w[u][3] = q.w;
                 }
             }
@@ -587,12 +596,13 @@ __global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
                 for (int c = top >= bound ? 0 : chunks;; ++c) {
                     while (c < chunks && of_chunk[c % kRemember][tid] < bound) ++c;
                     if (!__any_sync(kFull, c < chunks)) break;
-                    const int first = c * kChunk + tid;
+                    const int first = c * kChunk + tid - skip;
                     uint4 q[kU];
 #pragma unroll
                     for (int u = 0; u < kU; ++u) {
                         q[u] = make_uint4(Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill, Elem<T>::kFill);
-                        if (c < chunks && first + u * TH < p.nv) q[u] = vectors[first + u * TH];
+                        if (c < chunks && first + u * TH < p.nv && (u > 0 || first >= 0))
+                            q[u] = vectors[first + u * TH];
                     }
 #pragma unroll
                     for (int u = 0; u < kU; ++u) {
