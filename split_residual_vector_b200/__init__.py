@@ -11,6 +11,7 @@ this module raises.
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import os
 
@@ -371,20 +372,30 @@ TokenLogprobs = collections.namedtuple("TokenLogprobs",
                                        "logprob entropy lse top_ids top_logprob")
 TokenLogprobs.__doc__ = """Values of token_logprobs: logprob, entropy, lse [S(, n)] float32,
 top_ids [S(, n), k] int32 and top_logprob [S(, n), k] float32; None where not wanted."""
-_NO_VALUES = TokenLogprobs(None, None, None, None, None)
 
 
-def _call_on(device, stream, call):
-    """call(raw stream) on `device` and `stream` (None: the device's current stream), which are
-    made current first where they are not, so that outputs are allocated there too."""
+@contextlib.contextmanager
+def _current(device, stream):
+    """`device` and `stream` (None: the device's current stream) made current, so that outputs
+    are allocated there too."""
     import torch
-    if stream is not None:
-        with torch.cuda.stream(stream), torch.cuda.device(device):
-            return call(stream.cuda_stream)
-    if device.index != torch.cuda.current_device():
+    if stream is None:
         with torch.cuda.device(device):
-            return call(torch.cuda.current_stream().cuda_stream)
-    return call(torch._C._cuda_getCurrentRawStream(device.index))
+            yield
+    else:
+        with torch.cuda.stream(stream), torch.cuda.device(device):
+            yield
+
+
+def _elsewhere(device, stream):
+    """Whether a call has to make its device or stream current first."""
+    import torch
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def _raw_stream(device):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _new_values(lead, device, tokens, top_k):
@@ -392,33 +403,37 @@ def _new_values(lead, device, tokens, top_k):
     import torch
     entropy = torch.empty(*lead, dtype=torch.float32, device=device)
     lse = torch.empty_like(entropy)
-    logprob = None if tokens is None else torch.empty_like(entropy)
-    ids = top = None
+    logprob = ids = top = p_logprob = p_ids = p_top = None
+    if tokens is not None:
+        logprob = torch.empty_like(entropy)
+        p_logprob = logprob.data_ptr()
     if top_k:
         top = torch.empty(*lead, top_k, dtype=torch.float32, device=device)
         ids = torch.empty_like(top, dtype=torch.int32)
-    v = TokenLogprobs(logprob, entropy, lse, ids, top)
-    return v, [None if t is None else t.data_ptr() for t in v]
+        p_ids, p_top = ids.data_ptr(), top.data_ptr()
+    return (TokenLogprobs(logprob, entropy, lse, ids, top),
+            (p_logprob, entropy.data_ptr(), lse.data_ptr(), p_ids, p_top))
 
 
 def _given_values(v, lead, device, top_k):
     """The same of outputs that the caller gave."""
     import torch
     f32, top = torch.float32, (*lead, top_k)
-    return v, [_row_array(v.logprob, lead, f32, device), _row_array(v.entropy, lead, f32, device),
+    return v, (_row_array(v.logprob, lead, f32, device), _row_array(v.entropy, lead, f32, device),
                _row_array(v.lse, lead, f32, device), _row_array(v.top_ids, top, torch.int32, device),
-               _row_array(v.top_logprob, top, f32, device)]
+               _row_array(v.top_logprob, top, f32, device))
 
 
 def _logit_rows(logits):
     """(lead shape, dtype flag, S, n, V, stride_s, stride_n) of [S, V] or [S, n, V] logits."""
-    assert logits.is_cuda and logits.dim() in (2, 3), "logits are [S, V] or [S, n, V] on CUDA"
     shape, stride = logits.shape, logits.stride()
-    assert shape[-1] <= 1 or stride[-1] == 1, "a row's logits are contiguous"
-    assert shape[-1] <= MAX_VOCAB, f"rows have at most {MAX_VOCAB} logits"
-    if logits.dim() == 2:
-        return shape[:1], _dtype_flag(logits), shape[0], 1, shape[1], stride[0], 0
-    return shape[:2], _dtype_flag(logits), shape[0], shape[1], shape[2], stride[0], stride[1]
+    dims, V = len(shape), shape[-1]
+    assert logits.is_cuda and dims in (2, 3), "logits are [S, V] or [S, n, V] on CUDA"
+    assert V <= 1 or stride[-1] == 1, "a row's logits are contiguous"
+    assert V <= MAX_VOCAB, f"rows have at most {MAX_VOCAB} logits"
+    if dims == 2:
+        return shape[:1], _dtype_flag(logits), shape[0], 1, V, stride[0], 0
+    return shape[:2], _dtype_flag(logits), shape[0], shape[1], V, stride[0], stride[1]
 
 
 def _row_tokens(tokens, lead, device):
@@ -469,17 +484,15 @@ def token_logprobs(logits, tokens=None, pad=-1, scale=1.0, top_k=0, out=None, n_
     counting tokens past V."""
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
     dev, top_k = logits.device, int(top_k)
-    tok = _row_tokens(tokens, lead, dev)
-
-    def call(raw):
-        v, pointers = (_new_values(lead, dev, tokens, max(top_k, 0)) if out is None
-                       else _given_values(out, lead, dev, top_k))
-        _check(library().mimi_rvq_token_logprob(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *tok, pad, scale, top_k, *pointers,
-            _bad_counter(n_bad, dev), raw), "mimi_rvq_token_logprob")
-        return v
-
-    return _call_on(dev, stream, call)
+    if _elsewhere(dev, stream):
+        with _current(dev, stream):
+            return token_logprobs(logits, tokens, pad, scale, top_k, out, n_bad)
+    v, pointers = (_new_values(lead, dev, tokens, max(top_k, 0)) if out is None
+                   else _given_values(out, lead, dev, top_k))
+    _check(library().mimi_rvq_token_logprob(
+        logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, lead, dev), pad, scale,
+        top_k, *pointers, _bad_counter(n_bad, dev), _raw_stream(dev)), "mimi_rvq_token_logprob")
+    return v
 
 
 def token_logprobs_grad(logits, tokens=None, g_logprob=None, g_entropy=None, g_lse=None, pad=-1,
@@ -492,21 +505,23 @@ def token_logprobs_grad(logits, tokens=None, g_logprob=None, g_entropy=None, g_l
     import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
     dev, f32 = logits.device, torch.float32
-    tok = _row_tokens(tokens, lead, dev)
-
-    def call(raw):
-        d, d_strides = _gradient(out, logits)
+    if _elsewhere(dev, stream):
+        with _current(dev, stream):
+            return token_logprobs_grad(logits, tokens, g_logprob, g_entropy, g_lse, pad, scale,
+                                       values, out, n_bad)
+    d, d_strides = _gradient(out, logits)
+    if not values:
+        v, pointers = None, (None, None, None)
+    else:
         v, pointers = (_new_values(lead, dev, tokens, 0) if values is True
-                       else _given_values(values or _NO_VALUES, lead, dev, 0))
+                       else _given_values(values, lead, dev, 0))
         assert v.top_ids is None and v.top_logprob is None, "the gradient call lists no tokens"
-        _check(library().mimi_rvq_token_logprob_grad(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *tok, pad, scale,
-            _row_array(g_logprob, lead, f32, dev), _row_array(g_entropy, lead, f32, dev),
-            _row_array(g_lse, lead, f32, dev), d.data_ptr(), *d_strides, *pointers[:3],
-            _bad_counter(n_bad, dev), raw), "mimi_rvq_token_logprob_grad")
-        return (d, v) if values else d
-
-    return _call_on(dev, stream, call)
+    _check(library().mimi_rvq_token_logprob_grad(
+        logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, lead, dev), pad, scale,
+        _row_array(g_logprob, lead, f32, dev), _row_array(g_entropy, lead, f32, dev),
+        _row_array(g_lse, lead, f32, dev), d.data_ptr(), *d_strides, *pointers[:3],
+        _bad_counter(n_bad, dev), _raw_stream(dev)), "mimi_rvq_token_logprob_grad")
+    return (d, v) if values else d
 
 
 def _teacher_list(ids, teacher, lead, device):
@@ -527,17 +542,15 @@ def distill_topk(logits, ids, teacher, tail=False, scale=1.0, out=None, n_bad=No
     import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
     dev, f32 = logits.device, torch.float32
-    lists = _teacher_list(ids, teacher, lead, dev)
-
-    def call(raw):
-        loss = torch.empty(*lead, dtype=f32, device=dev) if out is None else out
-        _check(library().mimi_rvq_distill_topk(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *lists, 1 if tail else 0, scale,
-            _row_array(loss, lead, f32, dev), _bad_counter(n_bad, dev), raw),
-            "mimi_rvq_distill_topk")
-        return loss
-
-    return _call_on(dev, stream, call)
+    if _elsewhere(dev, stream):
+        with _current(dev, stream):
+            return distill_topk(logits, ids, teacher, tail, scale, out, n_bad)
+    loss = torch.empty(*lead, dtype=f32, device=dev) if out is None else out
+    _check(library().mimi_rvq_distill_topk(
+        logits.data_ptr(), dt, S, n, V, ss, sn, *_teacher_list(ids, teacher, lead, dev),
+        1 if tail else 0, scale, _row_array(loss, lead, f32, dev), _bad_counter(n_bad, dev),
+        _raw_stream(dev)), "mimi_rvq_distill_topk")
+    return loss
 
 
 def distill_topk_grad(logits, ids, teacher, g=None, tail=False, scale=1.0, loss=None, out=None,
@@ -549,16 +562,15 @@ def distill_topk_grad(logits, ids, teacher, g=None, tail=False, scale=1.0, loss=
     import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
     dev, f32 = logits.device, torch.float32
-    lists = _teacher_list(ids, teacher, lead, dev)
-
-    def call(raw):
-        d, d_strides = _gradient(out, logits)
-        losses = torch.empty(*lead, dtype=f32, device=dev) if loss is True else loss
-        _check(library().mimi_rvq_distill_topk_grad(
-            logits.data_ptr(), dt, S, n, V, ss, sn, *lists, 1 if tail else 0, scale,
-            _row_array(g, lead, f32, dev), d.data_ptr(), *d_strides,
-            _row_array(losses, lead, f32, dev), _bad_counter(n_bad, dev), raw),
-            "mimi_rvq_distill_topk_grad")
-        return d if losses is None else (d, losses)
-
-    return _call_on(dev, stream, call)
+    if _elsewhere(dev, stream):
+        with _current(dev, stream):
+            return distill_topk_grad(logits, ids, teacher, g, tail, scale, loss, out, n_bad)
+    d, d_strides = _gradient(out, logits)
+    if loss is True:
+        loss = torch.empty(*lead, dtype=f32, device=dev)
+    _check(library().mimi_rvq_distill_topk_grad(
+        logits.data_ptr(), dt, S, n, V, ss, sn, *_teacher_list(ids, teacher, lead, dev),
+        1 if tail else 0, scale, _row_array(g, lead, f32, dev), d.data_ptr(), *d_strides,
+        _row_array(loss, lead, f32, dev), _bad_counter(n_bad, dev), _raw_stream(dev)),
+        "mimi_rvq_distill_topk_grad")
+    return d if loss is None else (d, loss)
