@@ -566,7 +566,7 @@ __device__ __forceinline__ int group_in_block() { return TH < block_of<TH>() ? t
 // ------------------------------------------------------------------ host side
 
 constexpr int kShortBytes = 8192;           // longest row of half a warp or a warp
-constexpr int kPartBytes = 72 * 1024;       // a CTA's share that leaves room for three a SM
+constexpr int kPartBytes = 110 * 1024;      // a CTA's share that leaves room for two a SM
 constexpr int kSmemBytes = 227 * 1024;
 
 struct Shape {
@@ -574,10 +574,13 @@ struct Shape {
 };
 
 // Threads and CTAs for a row of V elements: `few` threads up to 8 KB; else a CTA of 128 or 256.
-// Rows over 72 KB that have to lie in shared memory whole, and rows of a batch that would leave
+// Rows over 110 KB that have to lie in shared memory whole, and rows of a batch that would leave
 // SMs idle, are split over a cluster of up to 8 CTAs; rows that only pass through until there are
 // 4 CTAs a SM, as each has 24 KB on its way (100 rows of 131072 float32 logits: 20.4 us unsplit, 9.8
 // in fours; rows that lie whole gain nothing: 148 of 32000 take 8.4 us as pairs, 12.5 in fours).
+// 110 KB: what a cluster's barriers cost is more than a third CTA a SM gains, and one CTA alone
+// does not hide its own turns. 2000 rows of 100 KB, distillation and its gradient: 85 and 132 us
+// as pairs, 50 and 93 in one CTA; 2000 of 120 KB, the gradient: 123 as pairs, 146 in one CTA.
 inline Shape shape_of(int64_t rows, int V, int size, int few, bool whole) {
     const int64_t bytes = (int64_t)V * size;
     if (few && bytes <= kShortBytes) return {few, 0};
