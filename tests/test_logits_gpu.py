@@ -124,7 +124,9 @@ def test_top_alternatives_of_ordinary_rows(V, dtype):
 
 @pytest.mark.parametrize("S,n,V,dtype", [(9001, 3, 65, BF16), (3000, 7, 130, F32), (2500, 0, 4104, BF16),
                                          (2500, 0, 4104, F32), (1500, 0, 17001, BF16), (700, 0, 20001, F32),
-                                         (130, 0, 70001, F32), (90, 0, 150001, BF16)])
+                                         (130, 0, 70001, F32), (90, 0, 150001, BF16),
+                                         (310, 0, 52001, BF16), (310, 0, 28001, F32),
+                                         (160, 0, 60001, BF16)])
 def test_many_rows(S, n, V, dtype):
     """More rows than are resident at once, so that every group walks several; among them rows
     without target, list or upstream gradient, and rows of NaN in their places."""
