@@ -133,7 +133,10 @@ int mimi_rvq_streams_wait_selftest(struct CUstream_st *stream);
  * distribution: lse and the logprob of a target are -inf, entropy is 0, its
  * gradient is 0. A row that holds NaN or +inf gives NaN for its values and its
  * gradient, and empty alternatives with logprob NaN. Where a row has no target
- * its logprob is 0 whatever its logits are.
+ * its logprob is 0 whatever its logits are. Logits of the type's lowest value
+ * are finite: a row of nothing else is uniform. A log probability beyond
+ * float32's range (such a logit times a scale above 1) is -inf, also where it
+ * enters a loss.
  *
  * Gradients: dlogits has the logits' type and its own strides; its rows must
  * not share memory, and it may be the logits themselves (same pointer and

@@ -324,6 +324,28 @@ def test_distillation_lists_that_go_wrong(V, dtype, tail):
     near(l2, loss, t_loss, "loss of weight 0")
 
 
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [6, 2048, 40000])
+def test_distillation_onto_the_lowest_logit(V, dtype, tail):
+    """A listed token masked by the type's lowest value: a finite loss while its log probability
+    is one in float32, infinite past it; the gradient is that of probability 0 either way."""
+    p = pkg()
+    x = make(3, 0, V, dtype, seed=60)
+    x[:, 1] = LOWEST[dtype]
+    ids = torch.tensor([[0, 1]] * 3, device="cuda", dtype=torch.int32)
+    t = torch.tensor([[0.5, 0.25]] * 3, device="cuda").log()
+    for c in (1.0, 2.0):
+        loss, t_loss, d, t_d = ref.distill(x, ids, t, tail=tail, c=c)
+        got_d, got = p.distill_topk_grad(x, ids, t, tail=tail, scale=c, loss=True)
+        near(got_d, d, t_d, "dlogits")
+        for v in (got, p.distill_topk(x, ids, t, tail=tail, scale=c)):
+            if c == 1.0:
+                near(v, loss, t_loss, "loss")
+            else:
+                assert (v == math.inf).all()
+
+
 def test_distillation_of_the_whole_vocabulary():
     """A list that holds every token: the tail class is left out, the student's own
     distribution gives a loss of rounding size and the gradient of the full KL."""
