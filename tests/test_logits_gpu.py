@@ -325,6 +325,21 @@ def test_distillation_lists_that_go_wrong(V, dtype, tail):
 
 
 @pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V", [6, 2048, 40000])
+def test_broken_entries_break_their_row(V, tail):
+    p = pkg()
+    x = make(4, 0, V, F32, seed=61)
+    ids = torch.tensor([[0, 1, -1]] * 4, device="cuda", dtype=torch.int32)
+    t = torch.full((4, 3), -1.5, device="cuda")
+    t[0, 1], t[2, 0], t[3, 2] = math.inf, math.nan, math.inf  # the last one's place is empty
+    d, l2 = p.distill_topk_grad(x, ids, t, tail=tail, loss=True)
+    for loss in (p.distill_topk(x, ids, t, tail=tail), l2):
+        assert torch.isnan(loss).tolist() == [True, False, True, False]
+    assert torch.isnan(d).all(-1).tolist() == [True, False, True, False]
+    assert torch.isfinite(d[1::2]).all()
+
+
+@pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("V", [6, 2048, 40000])
 def test_distillation_onto_the_lowest_logit(V, dtype, tail):
