@@ -1,0 +1,45 @@
+"""The calls on the streams' logits at the edges of what they allow: layouts that lie between one
+another, extreme logits and scales, optional arguments, and many rows with long lists."""
+import pytest
+
+torch = pytest.importorskip("torch")
+import logits_ref as ref  # noqa: E402
+from logits_ref import near  # noqa: E402
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def pkg():
+    import split_residual_vector_b200 as p
+    return p
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(shape, dtype, seed, spread=3.0):
+    return torch.empty(shape, device="cuda").normal_(0, spread, generator=gen(seed)).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [6, 2048, 6001, 140001])
+def test_tail_class_between_logits_of_opposite_sign(V, dtype):
+    """Listed logits near float32's largest value and the others near its lowest: the tail's log
+    probability is the scale times a difference that float32 does not hold."""
+    p = pkg()
+    x = normal((4, V), dtype, 1) * 1e30 - 3.0e38
+    ids = torch.stack([torch.randperm(V, device="cuda", generator=gen(i))[:4] for i in range(4)])
+    ids = ids.to(torch.int32)
+    x.scatter_(1, ids.long(), 3.0e38)
+    t = torch.tensor([[0.4, 0.2, 0.1, 0.05]] * 4, device="cuda").log()
+    for c in (0.5, 0.001):
+        loss, t_loss, d, t_d = ref.distill(x, ids, t, None, True, c)
+        assert torch.isfinite(loss).all() and (loss > 1e34).all()
+        near(p.distill_topk(x, ids, t, tail=True, scale=c), loss, t_loss, f"loss {c}")
+        got, l2 = p.distill_topk_grad(x, ids, t, tail=True, scale=c, loss=True)
+        near(l2, loss, t_loss, f"loss with gradient {c}")
+        near(got, d, t_d, f"dlogits {c}")
