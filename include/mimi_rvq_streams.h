@@ -140,7 +140,8 @@ int mimi_rvq_streams_wait_selftest(struct CUstream_st *stream);
  *
  * Gradients: dlogits has the logits' type and its own strides; its rows must
  * not share memory, and it may be the logits themselves (same pointer and
- * strides) but may not overlap them in another way (EINVAL). Each value is
+ * strides) but may not overlap them in another way (EINVAL; where the two lie
+ * in each other's extent they need the same strides too). Each value is
  * computed in float32 and rounded once. A row whose upstream gradients are
  * all 0 gets zeros, whatever its logits are.
  *

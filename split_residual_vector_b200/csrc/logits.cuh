@@ -629,16 +629,35 @@ inline bool rows_apart(int64_t S, int n, int V, int64_t ss, int64_t sn) {
     return ss >= V && sn >= ss * (S - 1) + V;
 }
 
-// The gradient may take the logits' own place (same pointer and strides) but may not overlap
-// them in another way.
+// Whether a row at offset d from one of m rows of V elements, p >= V apart, and the m - 1 rows
+// after it on the same stride share an element with them.
+inline bool rows_meet(int64_t d, int64_t p, int64_t m, int64_t V) {
+    const int64_t q = d / p - (d % p < 0), r = d - q * p;
+    return (r < V && q < m && q > -m) || (r > p - V && q + 1 < m && q + 1 > -m);
+}
+
+// The gradient may take the logits' own place (same pointer and strides), or places between the
+// logits' rows (same strides: two column ranges of one buffer, every other stream), but may not
+// share elements with them in another way.
 inline bool apart_or_same(const void* x, int64_t ss, int64_t sn, const void* d, int64_t dss,
                           int64_t dsn, int64_t S, int n, int V, int size) {
-    if (x == d) return (S <= 1 || ss == dss) && (n <= 1 || sn == dsn);
+    const bool same = (S <= 1 || ss == dss) && (n <= 1 || sn == dsn);
+    if (x == d) return same;
     const char* a = static_cast<const char*>(x);
     const char* b = static_cast<const char*>(d);
     const char* a1 = a + (ss * (S - 1) + sn * (n - 1) + V) * size;
     const char* b1 = b + (dss * (S - 1) + dsn * (n - 1) + V) * size;
-    return a1 <= b || b1 <= a;
+    if (a1 <= b || b1 <= a) return true;
+    if (!same) return false;
+    // blocks of the smaller stride's rows, the larger stride apart (rows_apart holds for both)
+    int64_t P = S > 1 ? ss : V, M = S, p = n > 1 ? sn : V, m = n;
+    if (M == 1 || (m > 1 && p > P)) {
+        int64_t t = P; P = p; p = t;
+        t = M; M = m; m = t;
+    }
+    const int64_t off = (b - a) / size, q = off / P - (off % P < 0), r = off - q * P;
+    return !(q < M && q > -M && rows_meet(r, p, m, V)) &&
+           !(q + 1 < M && q + 1 > -M && rows_meet(r - P, p, m, V));
 }
 
 // One launch over all rows: as many groups as are resident, each with `slots` places of 16 bytes

@@ -82,3 +82,63 @@ def test_logits_over_the_whole_range_at_tiny_scales(V, dtype):
             near(p.distill_topk(x, ids, t, tail=tail, scale=c), loss, t_loss, f"loss {tail}")
             got = p.distill_topk_grad(x, ids, t, one * 1e37, tail=tail, scale=c)
             near(got, d, t_d, f"distillation dlogits {tail}")
+
+
+def interleaved(S, n, V, dtype):
+    """(name, x, d): views [S, n, V] of one buffer that share no element."""
+    def two(shape, pick):
+        buf = normal(shape, dtype, 3)
+        return pick(buf)
+
+    yield "beside each other", *two((S, n, 2, V), lambda b: (b[:, :, 0], b[:, :, 1]))
+    yield "and the other way", *two((S, n, 2, V), lambda b: (b[:, :, 1], b[:, :, 0]))
+    yield "column ranges", *two((S, n, 2 * V + 7), lambda b: (b[..., 3:3 + V], b[..., V + 5:2 * V + 5]))
+    yield "halves of the streams", *two((S, 2 * n, V), lambda b: (b[:, :n], b[:, n:]))
+    yield "every other stream", *two((S, 2 * n, V), lambda b: (b[:, ::2], b[:, 1::2]))
+    yield "every other step", *two((2 * S, n, V), lambda b: (b[1::2], b[::2]))
+    yield "stream by stream", *two((n, S, 2, V), lambda b: (b[:, :, 0].transpose(0, 1),
+                                                            b[:, :, 1].transpose(0, 1)))
+    # steps that are no whole number of rows apart
+    def padded(b):
+        return (b.as_strided((S, n, V), (2 * n * V + 11, 2 * V, 1)),
+                b.as_strided((S, n, V), (2 * n * V + 11, 2 * V, 1), V))
+    yield "padded steps", *two((S * (2 * n * V + 11) + V,), padded)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("S,n,V", [(1, 1, 40), (1, 3, 100), (5, 1, 33), (6, 4, 2049), (3, 2, 9000)])
+def test_gradients_between_the_logits_rows(S, n, V, dtype):
+    p = pkg()
+    tok = torch.randint(0, V, (S, n), device="cuda", generator=gen(4), dtype=torch.int32)
+    g = torch.randn((S, n), device="cuda", generator=gen(5))
+    ids = torch.randint(0, V, (S, n, 3), device="cuda", generator=gen(6), dtype=torch.int32)
+    t = torch.full((S, n, 3), -1.5, device="cuda")
+    for name, x, d in interleaved(S, n, V, dtype):
+        kept = x.clone()
+        assert p.token_logprobs_grad(x, tok, g, g, out=d) is d
+        near(d, *ref.logprob_grad(kept, tok, g, g), name)
+        assert torch.equal(x, kept), name
+        p.distill_topk_grad(x, ids, t, g, tail=True, out=d)
+        near(d, *ref.distill(kept, ids, t, g, True)[2:], name)
+        assert torch.equal(x, kept), name
+
+
+def test_gradients_that_share_elements_with_the_logits_are_refused():
+    p = pkg()
+    S, n, V = 4, 3, 50
+    tok = torch.zeros((S, n), device="cuda", dtype=torch.int32)
+    g = torch.ones((S, n), device="cuda")
+    ids, t = tok.unsqueeze(-1), torch.zeros((S, n, 1), device="cuda")
+    buf = torch.zeros(8 * S * n * V, device="cuda")
+    view = lambda ss, sn, at: buf.as_strided((S, n, V), (ss, sn, 1), at)  # noqa: E731
+    P, q = 2 * n * V, 2 * V
+    for x, d in ((view(P, q, 0), view(P, q, V - 1)), (view(P, q, 0), view(P, q, V + 1)),
+                 (view(P, q, V), view(P, q, 1)), (view(P, q, 0), view(P, q, 2 * V)),
+                 (view(P, q, 0), view(P, q, P)), (view(P, q, 0), view(P + V, q, V)),
+                 (view(P, q, V), view(P, V, 0)),
+                 (view(P - V, q, 0), view(P - V, q, V)),   # a step's last row meets the next step
+                 (view(P - V, q, V), view(P - V, q, 0))):
+        with pytest.raises(p.MimiRVQError):
+            p.token_logprobs_grad(x, tok, g, out=d)
+        with pytest.raises(p.MimiRVQError):
+            p.distill_topk_grad(x, ids, t, g, out=d)
