@@ -383,6 +383,7 @@ def _current(device, stream):
         with torch.cuda.device(device):
             yield
     else:
+        assert stream.device == device, "the stream belongs to another device than the logits"
         with torch.cuda.stream(stream), torch.cuda.device(device):
             yield
 
