@@ -569,6 +569,8 @@ def distill_topk_grad(logits, ids, teacher, g=None, tail=False, scale=1.0, loss=
     d, d_strides = _gradient(out, logits)
     if loss is True:
         loss = torch.empty(*lead, dtype=f32, device=dev)
+    elif loss is False:
+        loss = None
     _check(library().mimi_rvq_distill_topk_grad(
         logits.data_ptr(), dt, S, n, V, ss, sn, *_teacher_list(ids, teacher, lead, dev),
         1 if tail else 0, scale, _row_array(g, lead, f32, dev), d.data_ptr(), *d_strides,

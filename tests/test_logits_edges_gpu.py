@@ -142,3 +142,12 @@ def test_gradients_that_share_elements_with_the_logits_are_refused():
             p.token_logprobs_grad(x, tok, g, out=d)
         with pytest.raises(p.MimiRVQError):
             p.distill_topk_grad(x, ids, t, g, out=d)
+
+
+def test_losses_that_are_not_wanted():
+    p = pkg()
+    x = normal((3, 50), F32, 7)
+    ids = torch.zeros((3, 1), device="cuda", dtype=torch.int32)
+    t = torch.zeros((3, 1), device="cuda")
+    d = p.distill_topk_grad(x, ids, t, loss=False)
+    assert torch.equal(d, p.distill_topk_grad(x, ids, t))
