@@ -29,7 +29,7 @@ EXPORTS = ("mimi_rvq_create", "mimi_rvq_destroy", "mimi_rvq_encode", "mimi_rvq_e
            "mimi_rvq_encode_noalloc", "mimi_rvq_streams_get_error",
            "mimi_rvq_streams_wait_selftest", "mimi_rvq_token_logprob",
            "mimi_rvq_token_logprob_grad", "mimi_rvq_distill_topk", "mimi_rvq_distill_topk_grad")
-MAX_TOP, MAX_VOCAB = 128, 3 << 17
+MAX_TOP, MAX_VOCAB, MAX_LOGIT_STREAMS = 128, 3 << 17, 65536
 TEXT_CARD, TEXT_PAD, AUDIO_PAD = 32000, 32000, 2048
 
 _lib = None
@@ -399,6 +399,13 @@ def _raw_stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _list_length(k, what):
+    """k, refused here where the C argument would not hold it (or an output would be large)."""
+    if not 0 <= k <= MAX_TOP:
+        raise MimiRVQError(-1, what)
+    return k
+
+
 def _new_values(lead, device, tokens, top_k):
     """Outputs of token_logprobs and their pointers."""
     import torch
@@ -432,19 +439,21 @@ def _logit_rows(logits):
     assert logits.is_cuda and dims in (2, 3), "logits are [S, V] or [S, n, V] on CUDA"
     assert V <= 1 or stride[-1] == 1, "a row's logits are contiguous"
     assert V <= MAX_VOCAB, f"rows have at most {MAX_VOCAB} logits"
+    assert dims == 2 or shape[1] <= MAX_LOGIT_STREAMS, f"at most {MAX_LOGIT_STREAMS} streams"
     if dims == 2:
         return shape[:1], _dtype_flag(logits), shape[0], 1, V, stride[0], 0
     return shape[:2], _dtype_flag(logits), shape[0], shape[1], V, stride[0], stride[1]
 
 
-def _row_tokens(tokens, lead, device):
-    """(pointer, stride_s, stride_n) of tokens of the rows' shape, any strides."""
+def _row_tokens(tokens, pad, lead, device):
+    """(pointer, stride_s, stride_n, pad) of tokens of the rows' shape, any strides."""
     import torch
+    assert -(1 << 31) <= pad < 1 << 31, "pad is an int32"
     if tokens is None:
-        return None, 0, 0
+        return None, 0, 0, pad
     assert tokens.dtype == torch.int32 and tokens.shape == lead and tokens.device == device
     st = tokens.stride()
-    return tokens.data_ptr(), st[0], st[1] if len(st) == 2 else 0
+    return tokens.data_ptr(), st[0], st[1] if len(st) == 2 else 0, pad
 
 
 def _row_array(t, shape, dtype, device):
@@ -484,14 +493,14 @@ def token_logprobs(logits, tokens=None, pad=-1, scale=1.0, top_k=0, out=None, n_
     place of values that are not wanted. n_bad: optional CUDA int64 [1] (caller-zeroed)
     counting tokens past V."""
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
-    dev, top_k = logits.device, int(top_k)
+    dev, top_k = logits.device, _list_length(int(top_k), "mimi_rvq_token_logprob")
     if _elsewhere(dev, stream):
         with _current(dev, stream):
             return token_logprobs(logits, tokens, pad, scale, top_k, out, n_bad)
-    v, pointers = (_new_values(lead, dev, tokens, max(top_k, 0)) if out is None
+    v, pointers = (_new_values(lead, dev, tokens, top_k) if out is None
                    else _given_values(out, lead, dev, top_k))
     _check(library().mimi_rvq_token_logprob(
-        logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, lead, dev), pad, scale,
+        logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, pad, lead, dev), scale,
         top_k, *pointers, _bad_counter(n_bad, dev), _raw_stream(dev)), "mimi_rvq_token_logprob")
     return v
 
@@ -518,7 +527,7 @@ def token_logprobs_grad(logits, tokens=None, g_logprob=None, g_entropy=None, g_l
                        else _given_values(values, lead, dev, 0))
         assert v.top_ids is None and v.top_logprob is None, "the gradient call lists no tokens"
     _check(library().mimi_rvq_token_logprob_grad(
-        logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, lead, dev), pad, scale,
+        logits.data_ptr(), dt, S, n, V, ss, sn, *_row_tokens(tokens, pad, lead, dev), scale,
         _row_array(g_logprob, lead, f32, dev), _row_array(g_entropy, lead, f32, dev),
         _row_array(g_lse, lead, f32, dev), d.data_ptr(), *d_strides, *pointers[:3],
         _bad_counter(n_bad, dev), _raw_stream(dev)), "mimi_rvq_token_logprob_grad")
@@ -529,7 +538,7 @@ def _teacher_list(ids, teacher, lead, device):
     """(ids, teacher, teacher dtype, k) of a teacher's lists [S(, n), k]."""
     import torch
     assert ids.dim() == len(lead) + 1 and teacher.dtype in (torch.float32, torch.bfloat16)
-    shape = (*lead, ids.shape[-1])
+    shape = (*lead, _list_length(ids.shape[-1], "mimi_rvq_distill_topk"))
     return (_row_array(ids, shape, torch.int32, device),
             _row_array(teacher, shape, teacher.dtype, device), _dtype_flag(teacher), shape[-1])
 

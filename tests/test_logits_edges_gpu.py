@@ -151,3 +151,22 @@ def test_losses_that_are_not_wanted():
     t = torch.zeros((3, 1), device="cuda")
     d = p.distill_topk_grad(x, ids, t, loss=False)
     assert torch.equal(d, p.distill_topk_grad(x, ids, t))
+
+
+def test_arguments_past_the_calls_integers():
+    """Sizes that a 32-bit argument would not hold are refused, not taken modulo 2^32."""
+    p = pkg()
+    x = normal((2, 50), F32, 8)
+    tok = torch.full((2,), 5, device="cuda", dtype=torch.int32)
+    for pad in ((1 << 32) + 5, -(1 << 32) + 5, 1 << 31):
+        with pytest.raises(AssertionError):
+            p.token_logprobs(x, tok, pad=pad)
+        with pytest.raises(AssertionError):
+            p.token_logprobs_grad(x, tok, torch.ones(2, device="cuda"), pad=pad)
+    for pad in ((1 << 31) - 1, -(1 << 31)):
+        assert p.token_logprobs(x, tok, pad=pad).logprob.all()
+    wide = x[:1, :1].view(1, 1, 1).expand(1, (1 << 32) + 1, 1)[:, :, :1]
+    with pytest.raises(AssertionError):
+        p.token_logprobs(wide, out=p.TokenLogprobs(None, None, None, None, None))
+    with pytest.raises(p.MimiRVQError):
+        p.token_logprobs(x[:0], tok[:0], top_k=(1 << 32) + 1)
