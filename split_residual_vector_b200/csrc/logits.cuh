@@ -661,9 +661,10 @@ inline bool apart_or_same(const void* x, int64_t ss, int64_t sn, const void* d, 
 }
 
 // One launch over all rows: as many groups as are resident, each with `slots` places of 16 bytes
-// in dynamic shared memory, or one for each row if they are fewer.
-// kMore: threads of a CTA beside the row's TH.
-template <auto kernel, int TH, int kMore, typename... Args>
+// in dynamic shared memory, or one for each row if they are fewer (rows are dealt out to the whole
+// grid from the start, so a CTA that has to wait for another's end would hold its rows back).
+// kMore: threads of a CTA beside the row's TH; kPerSm: CTAs per SM the kernel is compiled for.
+template <auto kernel, int TH, int kMore, int kPerSm, typename... Args>
 cudaError_t launch_rows(const RowsIn& in, int static_smem, cudaStream_t stream, Args... args) {
     constexpr int block = block_of<TH>() + kMore, rows_per = block_of<TH>() / TH;
     const int smem = rows_per * in.slots * 16;
@@ -679,7 +680,7 @@ cudaError_t launch_rows(const RowsIn& in, int static_smem, cudaStream_t stream, 
         if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELAXED);
     }
     int per_sm = (kSmemBytes + 1024) / (smem + static_smem + 1024);
-    if (per_sm > blocks_of<TH>()) per_sm = blocks_of<TH>();
+    if (per_sm > kPerSm) per_sm = kPerSm;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     const int64_t groups = (in.rows + rows_per - 1) / rows_per;
     int64_t most = ((int64_t)sms * per_sm) >> in.log_cluster;

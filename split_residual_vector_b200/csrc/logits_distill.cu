@@ -497,12 +497,18 @@ __global__ void __launch_bounds__(block_of<TH>() + lister_of<TH>(), distill_bloc
     }
 }
 
+template <typename T, int TH, bool kGrad>
+cudaError_t launch_distill(const RowsIn& in, const TeacherIn& te, cudaStream_t s) {
+    return launch_rows<&k_distill<T, TH, kGrad>, TH, lister_of<TH>(), distill_blocks<TH>()>(
+        in, 1024, s, in, te);
+}
+
 template <typename T, bool kGrad>
 cudaError_t distill_of(int threads, const RowsIn& in, const TeacherIn& te, cudaStream_t s) {
     switch (threads) {
-        case 16: return launch_rows<&k_distill<T, 16, kGrad>, 16, lister_of<16>()>(in, 1024, s, in, te);
-        case 128: return launch_rows<&k_distill<T, 128, kGrad>, 128, lister_of<128>()>(in, 1024, s, in, te);
-        default: return launch_rows<&k_distill<T, 256, kGrad>, 256, lister_of<256>()>(in, 1024, s, in, te);
+        case 16: return launch_distill<T, 16, kGrad>(in, te, s);
+        case 128: return launch_distill<T, 128, kGrad>(in, te, s);
+        default: return launch_distill<T, 256, kGrad>(in, te, s);
     }
 }
 

@@ -403,9 +403,10 @@ __global__ void __launch_bounds__(block_of<TH>(), blocks_of<TH>())
 // and reads its own places of a ring of kStages chunks of kU vectors a thread; copies run
 // kStages - 1 chunks ahead, across rows.
 constexpr int kLong = 128, kU = 4, kStages = 3, kChunk = kU * kLong, kRemember = 8;
+__host__ __device__ constexpr int long_blocks(bool top) { return top ? 6 : blocks_of<kLong>(); }
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLong, kTop ? 6 : blocks_of<kLong>())
+__global__ void __launch_bounds__(kLong, long_blocks(kTop))
     k_logprob_long(RowsIn in, TokensIn tk, ValuesOut o) {
     constexpr int TH = kLong, kPer = Elem<T>::kPer, kPairs = kPer / 2;
     extern __shared__ uint4 ring[];  // [kStages][kU][TH], then TopLists in a cluster
@@ -775,19 +776,24 @@ cudaError_t forward_of(int threads, const RowsIn& in, const TokensIn& tk, const 
                        cudaStream_t s) {
     constexpr int kShort = kTop ? 32 : 16;
     if (threads == kShort)  // the last figures: static shared memory, rounded up
-        return launch_rows<&k_logprob<T, kShort, kTop>, kShort, 0>(in, kTop ? 12 * 1024 : 512, s, in, tk, o);
+        return launch_rows<&k_logprob<T, kShort, kTop>, kShort, 0, blocks_of<kShort>()>(
+            in, kTop ? 12 * 1024 : 512, s, in, tk, o);
     RowsIn with_ring = in;
     with_ring.slots = kStages * kChunk + (kTop && in.log_cluster ? (int)sizeof(TopLists) / 16 + 1 : 0);
-    return launch_rows<&k_logprob_long<T, kTop>, kLong, 0>(with_ring, kTop ? 11 * 1024 : 1024, s, with_ring, tk, o);
+    return launch_rows<&k_logprob_long<T, kTop>, kLong, 0, long_blocks(kTop)>(
+        with_ring, kTop ? 11 * 1024 : 1024, s, with_ring, tk, o);
 }
 
 template <typename T>
 cudaError_t gradient_of(int threads, const RowsIn& in, const TokensIn& tk, const GradIn& g,
                         const ValuesOut& o, cudaStream_t s) {
     switch (threads) {
-        case 16: return launch_rows<&k_logprob_grad<T, 16>, 16, 0>(in, 1024, s, in, tk, g, o);
-        case 128: return launch_rows<&k_logprob_grad<T, 128>, 128, 0>(in, 1024, s, in, tk, g, o);
-        default: return launch_rows<&k_logprob_grad<T, 256>, 256, 0>(in, 1024, s, in, tk, g, o);
+        case 16: return launch_rows<&k_logprob_grad<T, 16>, 16, 0, blocks_of<16>()>(
+            in, 1024, s, in, tk, g, o);
+        case 128: return launch_rows<&k_logprob_grad<T, 128>, 128, 0, blocks_of<128>()>(
+            in, 1024, s, in, tk, g, o);
+        default: return launch_rows<&k_logprob_grad<T, 256>, 256, 0, blocks_of<256>()>(
+            in, 1024, s, in, tk, g, o);
     }
 }
 

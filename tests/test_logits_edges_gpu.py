@@ -170,3 +170,50 @@ def test_arguments_past_the_calls_integers():
         p.token_logprobs(wide, out=p.TokenLogprobs(None, None, None, None, None))
     with pytest.raises(p.MimiRVQError):
         p.token_logprobs(x[:0], tok[:0], top_k=(1 << 32) + 1)
+
+
+GRIDS = [(4000, 0, 12000, BF16, 8), (4000, 0, 5000, F32, 8), (2000, 8, 2048, BF16, 64),
+         (2000, 8, 2048, BF16, 20), (2000, 8, 300, F32, 100), (3000, 0, 3000, F32, 33),
+         (2000, 0, 20000, BF16, 128), (1500, 0, 32000, BF16, 64)]
+
+
+@pytest.mark.parametrize("S,n,V,dtype,k", GRIDS)
+def test_grids_of_many_rows_are_resident(S, n, V, dtype, k):
+    """Rows are dealt out to the CTAs of the grid, so every CTA has to run from the start: the
+    grid of a captured launch is compared with the CTAs the driver says fit."""
+    driver = pytest.importorskip("cuda.bindings.driver")
+    p = pkg()
+    x = normal((S, max(n, 1), V), dtype, 9)
+    x = x if n else x[:, 0]
+    lead = x.shape[:-1]
+    tok = torch.zeros(lead, device="cuda", dtype=torch.int32)
+    ids = torch.randint(0, V, (*lead, k), device="cuda", generator=gen(10), dtype=torch.int32)
+    t = torch.full(ids.shape, -6.0, device="cuda")
+    g = torch.ones(lead, device="cuda")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+
+    def ok(result):
+        assert result[0] == driver.CUresult.CUDA_SUCCESS, result[0]
+        return result[1:]
+
+    for name, call in (("values", lambda: p.token_logprobs(x, tok)),
+                       ("alternatives", lambda: p.token_logprobs(x, tok, top_k=k)),
+                       ("gradient", lambda: p.token_logprobs_grad(x, tok, g)),
+                       ("loss", lambda: p.distill_topk(x, ids, t)),
+                       ("loss's gradient", lambda: p.distill_topk_grad(x, ids, t, g))):
+        call()
+        graph = torch.cuda.CUDAGraph(keep_graph=True)
+        with torch.cuda.graph(graph):
+            call()
+        raw = driver.CUgraph(graph.raw_cuda_graph())
+        (count,) = ok(driver.cuGraphGetNodes(raw))[1:]
+        nodes = ok(driver.cuGraphGetNodes(raw, count))[0]
+        assert len(nodes) == 1, name
+        (node,) = ok(driver.cuGraphKernelNodeGetParams(nodes[0]))
+        func = node.func
+        if int(func) == 0:
+            (func,) = ok(driver.cuKernelGetFunction(node.kern))
+        (fit,) = ok(driver.cuOccupancyMaxActiveBlocksPerMultiprocessor(func, node.blockDimX,
+                                                                       node.sharedMemBytes))
+        assert node.gridDimX <= fit * sms, f"{name}: {node.gridDimX} CTAs, {fit} fit an SM"
+        del graph
