@@ -556,9 +556,10 @@ __device__ __forceinline__ Stats join_row(Joint<TH>& j, Stats st, int tid, int c
 // Threads of a CTA: groups of short rows share one.
 template <int TH>
 __host__ __device__ constexpr int block_of() { return TH > 128 ? TH : 128; }
-// CTAs per SM a kernel is compiled for: 64 registers a thread
+// CTAs per SM that log probabilities of rows in shared memory and their gradient are compiled for:
+// 64 registers a thread. (Those of longer rows and distillation have figures of their own.)
 template <int TH>
-__host__ __device__ constexpr int blocks_of() { return TH == 384 ? 3 : 1024 / block_of<TH>(); }
+__host__ __device__ constexpr int blocks_of() { return 1024 / block_of<TH>(); }
 // A thread's number in its group, and its group's in the CTA.
 template <int TH>
 __device__ __forceinline__ int thread_in_group() { return TH < block_of<TH>() ? threadIdx.x % TH : threadIdx.x; }
