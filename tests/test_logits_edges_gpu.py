@@ -217,3 +217,38 @@ def test_grids_of_many_rows_are_resident(S, n, V, dtype, k):
                                                                        node.sharedMemBytes))
         assert node.gridDimX <= fit * sms, f"{name}: {node.gridDimX} CTAs, {fit} fit an SM"
         del graph
+
+
+@pytest.mark.parametrize("S,n,V,dtype", [(2500, 4, 300, BF16), (2500, 0, 2048, F32),
+                                         (1900, 0, 6000, BF16), (1300, 0, 6000, F32),
+                                         (1000, 0, 17001, BF16)])
+def test_many_rows_with_long_lists(S, n, V, dtype):
+    """Thousands of rows, so that every CTA walks several: ordinary rows between rows of few
+    distinct values, whose alternatives overflow the list, and between lists with ids twice."""
+    p = pkg()
+    x = normal((S, max(n, 1), V), dtype, 11)
+    few = torch.arange(S, device="cuda") % 3 == 1
+    x[few] = torch.randint(-3, 3, x[few].shape, device="cuda", generator=gen(12)).to(dtype)
+    x[torch.arange(S, device="cuda") % 7 == 2] = 1.5
+    x = x if n else x[:, 0]
+    lead = x.shape[:-1]
+    for k in (24, 33, 64, 100, 128):
+        r = p.token_logprobs(x, top_k=k)
+        ids, lp, tol = ref.top(x, k)
+        assert torch.equal(r.top_ids.reshape(ids.shape).long(), ids), k
+        near(r.top_logprob, lp, tol, f"top {k}")
+        del ids, lp, tol
+    g = torch.randn(lead, device="cuda", generator=gen(13))
+    for k in (20, 33, 64, 128):
+        ids = torch.randint(0, V, (*lead, k), device="cuda", generator=gen(14), dtype=torch.int32)
+        odd = torch.arange(S, device="cuda") % 2 == 1
+        ids[odd, ..., 3::5] = ids[odd, ..., 1:2]
+        ids[torch.arange(S, device="cuda") % 11 == 5] = -1
+        t = torch.log_softmax(torch.randn(ids.shape, device="cuda", generator=gen(15)), -1) - 0.1
+        for tail in (False, True):
+            loss, t_loss, d, t_d = ref.distill(x, ids, t, g, tail)
+            near(p.distill_topk(x, ids, t, tail=tail), loss, t_loss, f"loss {k}")
+            got, l2 = p.distill_topk_grad(x, ids, t, g, tail=tail, loss=True)
+            near(l2, loss, t_loss, f"loss with gradient {k}")
+            near(got, d, t_d, f"dlogits {k}")
+            del loss, d, t_d, got
