@@ -157,10 +157,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // Exponents t = log2(e) c (x - m) of a row's or warp's logits, 2^t = e^{c (x - m)}.
 // Near: t = x c2 - ref in one fused multiply-add per logit, ref = m c2 rounded; t is then off by
 // the same `shift` = m c2 - ref for every logit, at most 2^-9, which is taken back from the sums.
-// Far (logits or scales beyond that): the difference first, then the product; of half the logits
-// (exact) and twice c2, as logits of opposite sign may differ by more than float32 holds, which a
-// small scale brings back. With kFinite, t is at least -236 (2^t is 0 there too), so that 0 t is 0
-// for a logit of -inf; bf16 logits are clamped as pairs before they are widened.
+// Far (logits or scales beyond that): the difference first, then the product. With kFinite, t is
+// at least -236 (2^t is 0 there too), so that 0 t is 0 for a logit of -inf; bf16 logits are
+// clamped as pairs before they are widened.
 constexpr float kLow = -300.f;
 struct Scale {
     float c2, m, ref, shift;
@@ -198,10 +197,9 @@ __device__ __forceinline__ void exponents(const uint32_t (&w)[4], const Scale& k
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) t[j] = fma2(t[j], c, r);
     } else {
-        const Pair half = pair_of(0.5f, 0.5f), m = pair_of(-0.5f * k.m, -0.5f * k.m);
-        const Pair c = pair_of(2.f * k.c2, 2.f * k.c2);
+        const Pair c = pair_of(k.c2, k.c2), m = pair_of(-k.m, -k.m);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) t[j] = mul2(fma2(t[j], half, m), c);
+        for (int j = 0; j < kPairs; ++j) t[j] = mul2(add2(t[j], m), c);
     }
     if constexpr (kFinite && (sizeof(T) == 4 || kFar))
 #pragma unroll
@@ -213,7 +211,7 @@ __device__ __forceinline__ void exponents(const uint32_t (&w)[4], const Scale& k
 }
 // the same for one logit, without the near form
 __device__ __forceinline__ float exponent(float x, float m, float c2) {
-    return max_nan(fmaf(0.5f, x, m == -kInf ? 0.f : -0.5f * m) * (2.f * c2), kLow);
+    return max_nan((x - (m == -kInf ? 0.f : m)) * c2, kLow);
 }
 
 // ln of a sum (0: -inf) for gradients, within 2^-22 absolutely near 1; values take logf, as the

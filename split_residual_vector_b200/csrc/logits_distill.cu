@@ -286,7 +286,7 @@ __device__ __forceinline__ void put_rest(const Part<T>& p, const uint4* buf, int
     const Scale k(c2, w.rest.m);
     // a rest of -inf only has no gradient of its own: 2^t is 0 there
     const float f0 = gc * (w.Q * reciprocal(w.all.s)
-                               * (w.rest.s == 0.f ? 1.f : ex2(exponent(w.rest.m, w.all.m, c2)))
+                               * (w.rest.s == 0.f ? 1.f : ex2((w.rest.m - w.all.m) * c2))
                            - (w.qr > 0.f ? w.qr / w.rest.s : 0.f));
     const bool fast = !k.far && wide;
     const float f = fast ? f0 * ex2(-k.shift) : f0;
@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(block_of<TH>() + lister_of<TH>(), distill_bloc
         }
         parity ^= 1;
         w.all = Stats{fmaxf(w.rest.m, lm), 0.f, 0.f};
-        w.all.s = w.rest.s * ex2(exponent(w.rest.m, w.all.m, c2))
-                  + lsum * ex2(exponent(lm, w.all.m, c2));
+        const float mu = w.all.m == -kInf ? 0.f : w.all.m;
+        w.all.s = w.rest.s * ex2((w.rest.m - mu) * c2) + lsum * ex2((lm - mu) * c2);
         w.qr = w.rest.s == 0.f ? 0.f : ls.tail_q;
         w.Q = te.tail ? ls.Q + w.qr : ls.Q;
         return w;
