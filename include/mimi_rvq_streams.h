@@ -118,7 +118,7 @@ int mimi_rvq_streams_wait_selftest(struct CUstream_st *stream);
  * elements, >= 0; rows may start at any element, so the 16-byte rule does not
  * apply to logits and dlogits, nor to the other arrays of these calls, which
  * need their element's alignment). V in 1..MIMI_RVQ_MAX_VOCAB, n <= 65536. With
- * c = scale (> 0, at most 1e30; 1 / temperature):
+ * c = scale (1e-30 to 1e30; 1 / temperature):
  *     lse = ln sum_i exp(c x_i),  ln p_i = c x_i - lse,
  *     entropy = -sum_i p_i ln p_i   (0 ln 0 = 0).
  * Outputs other than dlogits are contiguous [S][n] (lists [S][n][k]) float32

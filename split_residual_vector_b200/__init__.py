@@ -489,9 +489,9 @@ def token_logprobs(logits, tokens=None, pad=-1, scale=1.0, top_k=0, out=None, n_
     (CUDA, rows contiguous, any strides between rows), tokens [S] or [S, n] int32 (a view such
     as packed[:, 1:9] is read in place; below 0 or equal to pad: no target, logprob 0).
     Returns TokenLogprobs; logprob is None without tokens, the top lists are None for
-    top_k = 0. scale is 1 / temperature. out: TokenLogprobs of tensors to write, None in the
-    place of values that are not wanted. n_bad: optional CUDA int64 [1] (caller-zeroed)
-    counting tokens past V."""
+    top_k = 0. scale is 1 / temperature (1e-30 to 1e30). out: TokenLogprobs of tensors to
+    write, None in the place of values that are not wanted. n_bad: optional CUDA int64 [1]
+    (caller-zeroed) counting tokens past V."""
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
     dev, top_k = logits.device, _list_length(int(top_k), "mimi_rvq_token_logprob")
     if _elsewhere(dev, stream):

@@ -168,7 +168,7 @@ struct Scale {
 
     __device__ Scale(float c2_, float m_) : c2(c2_), m(m_ == -kInf ? 0.f : m_) {
         ref = m * c2;
-        far = !(fabsf(ref) < 32768.f && c2 > 1.0e-33f && c2 < 1.0e30f);
+        far = !(fabsf(ref) < 32768.f && c2 < 1.0e30f);
         shift = far ? 0.f : fmaf(m, c2, -ref);
         const float f = __fdividef(ref + kLow, c2);
         floor_bf16x2 = pack_bf16x2(f, f);
@@ -616,7 +616,8 @@ inline bool rows_ok(int dtype, int64_t S, int n, int V, int64_t ss, int64_t sn, 
     if (S < 0 || n < 0 || n > 65536 || S > (int64_t(1) << 40)) return false;
     if (V < 1 || V > MIMI_RVQ_MAX_VOCAB || ss < 0 || sn < 0) return false;
     if ((__int128)ss * S + (__int128)sn * n > ((__int128)1 << 58)) return false;  // no offset wraps
-    return scale > 0.f && scale <= 1.0e30f;
+    // scales below 1e-30 would make ordinary exponents of differences past float32's range
+    return scale >= 1.0e-30f && scale <= 1.0e30f;
 }
 
 // Rows of a gradient must not share memory: the smaller stride holds a row, the larger one all

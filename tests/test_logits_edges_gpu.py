@@ -1,5 +1,5 @@
 """The calls on the streams' logits at the edges of what they allow: layouts that lie between one
-another, extreme logits, optional arguments, and many rows with long lists."""
+another, extreme logits and scales, optional arguments, and many rows with long lists."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -43,6 +43,47 @@ def test_tail_class_between_logits_of_opposite_sign(V, dtype):
         got, l2 = p.distill_topk_grad(x, ids, t, tail=True, scale=c, loss=True)
         near(l2, loss, t_loss, f"loss with gradient {c}")
         near(got, d, t_d, f"dlogits {c}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [5, 300, 2048, 9001, 140001])
+def test_logits_over_the_whole_range_at_the_smallest_scale(V, dtype):
+    """Differences of logits past float32's range: probability 0 at every scale that is taken."""
+    p = pkg()
+    x = (normal((4, V), F32, 2, 1.0e38).clamp(-3.3e38, 3.3e38)).to(dtype)
+    x[:, 0], x[:, V - 1] = 3.3e38, -3.3e38
+    x[2:] = normal((2, V), F32, 3, 1.0e30).to(dtype)  # ordinary exponents at this scale
+    tok = torch.tensor([0, V - 1, 1, V // 2], device="cuda", dtype=torch.int32)
+    c = torch.tensor(1e-30).item()
+    want = ref.logprob(x, tok, c=c)
+    r = p.token_logprobs(x, tok, scale=c, top_k=min(V, 9))
+    for name, (v, tol) in want.items():
+        near(getattr(r, name), v, tol, name)
+    ids, lp, tol = ref.top(x, min(V, 9), c)
+    assert torch.equal(r.top_ids.long(), ids[:, 0])
+    near(r.top_logprob, lp, tol, "top_logprob")
+    ids = torch.tensor([[0, V // 2, 2]] * 4, device="cuda", dtype=torch.int32)
+    t = torch.tensor([[0.4, 0.2, 0.1]] * 4, device="cuda").log()
+    g = torch.full((4,), 1e30, device="cuda")  # gradients that float32 holds
+    for tail in (False, True):
+        loss, t_loss, d, t_d = ref.distill(x, ids, t, g, tail, c)
+        near(p.distill_topk(x, ids, t, tail=tail, scale=c), loss, t_loss, f"loss {tail}")
+        near(p.distill_topk_grad(x, ids, t, g, tail=tail, scale=c), d, t_d, f"dlogits {tail}")
+
+
+@pytest.mark.parametrize("c", [9.9e-31, 1e-37, 1e-44])
+def test_smaller_scales_are_refused(c):
+    p = pkg()
+    x = normal((3, 50), F32, 4)
+    tok = torch.zeros(3, device="cuda", dtype=torch.int32)
+    g = torch.ones(3, device="cuda")
+    ids, t = tok.view(3, 1), g.view(3, 1)
+    for call in (lambda: p.token_logprobs(x, tok, scale=c),
+                 lambda: p.token_logprobs_grad(x, tok, g, scale=c),
+                 lambda: p.distill_topk(x, ids, t, scale=c),
+                 lambda: p.distill_topk_grad(x, ids, t, g, scale=c)):
+        with pytest.raises(p.MimiRVQError):
+            call()
 
 
 def interleaved(S, n, V, dtype):
