@@ -245,7 +245,7 @@ struct Lister {
             });
             part = lanes_sum<TH>(part);
             if (w.qr > 0.f)
-                part += w.qr * (logf(w.qr) - (log_prob(w.rest.m, c, w.all.m, ln_s) + logf(w.rest.s)));
+                part += w.qr * (logf(w.qr) - log_prob(w.rest.m, c, w.all.m, ln_s - logf(w.rest.s)));
         }
         if (me == 0) te.loss[r] = w.Q != w.Q ? NAN : part;
     }
