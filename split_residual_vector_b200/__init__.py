@@ -473,10 +473,15 @@ def _bad_counter(n_bad, device):
 
 
 def _gradient(out, logits):
-    """The gradient's tensor and its (stride_s, stride_n)."""
+    """The gradient's tensor and its (stride_s, stride_n). A new one is contiguous, or stream-major
+    where the logits are (its rows are then aligned as theirs, and stored as whole vectors)."""
     import torch
     if out is None:
-        out = torch.empty(*logits.shape, dtype=logits.dtype, device=logits.device)
+        shape = logits.shape
+        if len(shape) == 3 and logits.stride() == (shape[2], shape[0] * shape[2], 1):
+            out = torch.empty_like(logits)
+        else:
+            out = torch.empty(*shape, dtype=logits.dtype, device=logits.device)
     assert out.shape == logits.shape and out.dtype == logits.dtype and out.device == logits.device
     st = out.stride()
     assert out.shape[-1] <= 1 or st[-1] == 1
@@ -509,7 +514,8 @@ def token_logprobs_grad(logits, tokens=None, g_logprob=None, g_entropy=None, g_l
                         scale=1.0, values=None, out=None, n_bad=None, stream=None):
     """Gradient of sum(g_logprob * logprob + g_entropy * entropy + g_lse * lse) with respect to
     the logits, in the logits' type: g_* are [S] or [S, n] float32, None where there is none.
-    out may be the logits themselves. values = True, or a TokenLogprobs of tensors (top lists
+    out may be the logits themselves; a new gradient is contiguous, or stream-major where the
+    logits are dense and stream-major. values = True, or a TokenLogprobs of tensors (top lists
     None), also gives logprob, entropy and lse from the same pass: the call then returns
     (dlogits, TokenLogprobs). Otherwise it returns dlogits."""
     import torch
@@ -566,9 +572,10 @@ def distill_topk(logits, ids, teacher, tail=False, scale=1.0, out=None, n_bad=No
 def distill_topk_grad(logits, ids, teacher, g=None, tail=False, scale=1.0, loss=None, out=None,
                       n_bad=None, stream=None):
     """Gradient of sum(g * loss) with respect to the logits, in their type (g [S] or [S, n]
-    float32, None: all 1; out may be the logits themselves). loss = True, or a float32 tensor
-    [S] or [S, n], also gives the losses from the same pass: the call then returns
-    (dlogits, loss). Otherwise it returns dlogits."""
+    float32, None: all 1; out may be the logits themselves, a new gradient is laid out as
+    token_logprobs_grad's). loss = True, or a float32 tensor [S] or [S, n], also gives the
+    losses from the same pass: the call then returns (dlogits, loss). Otherwise (None, False)
+    it returns dlogits."""
     import torch
     lead, dt, S, n, V, ss, sn = _logit_rows(logits)
     dev, f32 = logits.device, torch.float32

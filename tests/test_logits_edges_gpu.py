@@ -221,6 +221,32 @@ def test_grids_of_many_rows_are_resident(S, n, V, dtype, k):
         del graph
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("S,n,V", [(10, 4, 2049), (1, 3, 50), (3, 1, 50), (4, 3, 1), (1, 1, 1),
+                                   (0, 3, 50), (4, 0, 50)])
+def test_new_gradients_are_laid_out_as_dense_logits(S, n, V, dtype):
+    """Stream-major logits give stream-major gradients, so that each row's alignment is the
+    logits' row's; all others, dense or not, contiguous ones."""
+    p = pkg()
+    dense = normal((n, S, V), dtype, 16).transpose(0, 1)
+    layouts = [("streams", dense, dense.stride()), ("plain", dense.contiguous(), None),
+               ("one row for all", normal((1, 1, V), dtype, 17).expand(S, n, V), None),
+               ("padded", normal((n, S, V + 3), dtype, 18)[:, :, :V].transpose(0, 1), None)]
+    for name, x, strides in layouts:
+        tok = torch.zeros((S, n), device="cuda", dtype=torch.int32)
+        g = torch.ones((S, n), device="cuda")
+        d = p.token_logprobs_grad(x, tok, g)
+        e = p.distill_topk_grad(x, tok.unsqueeze(-1), g.unsqueeze(-1), g)
+        for out in (d, e):
+            if strides is not None and S and n:
+                assert out.stride() == strides, name
+            else:
+                assert out.is_contiguous() or 1 in (S, n, V), name
+        if S and n:
+            near(d, *ref.logprob_grad(x, tok, g), name)
+            near(e, *ref.distill(x, tok.unsqueeze(-1), g.unsqueeze(-1), g)[2:], name)
+
+
 @pytest.mark.parametrize("S,n,V,dtype", [(2500, 4, 300, BF16), (2500, 0, 2048, F32),
                                          (1900, 0, 6000, BF16), (1300, 0, 6000, F32),
                                          (1000, 0, 17001, BF16)])
