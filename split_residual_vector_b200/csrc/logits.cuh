@@ -662,7 +662,9 @@ inline bool apart_or_same(const void* x, int64_t ss, int64_t sn, const void* d, 
 
 // One launch over all rows: as many groups as are resident, each with `slots` places of 16 bytes
 // in dynamic shared memory, or one for each row if they are fewer (rows are dealt out to the whole
-// grid from the start, so a CTA that has to wait for another's end would hold its rows back).
+// grid from the start, so a CTA that has to wait for another's end would hold its rows back). Of
+// clusters the device may run a few less than their shared memory allows (48 of 55 by eights):
+// a grid of exactly those took the same time.
 // kMore: threads of a CTA beside the row's TH; kPerSm: CTAs per SM the kernel is compiled for.
 template <auto kernel, int TH, int kMore, int kPerSm, typename... Args>
 cudaError_t launch_rows(const RowsIn& in, int static_smem, cudaStream_t stream, Args... args) {

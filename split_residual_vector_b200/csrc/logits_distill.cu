@@ -19,7 +19,7 @@
 // of its own, so that the row's threads hold no registers for its list and weigh
 // nothing while they could be adding: gradient of 3750 x 32000 bf16 rows with 64
 // entries 97 to 102 us (in the first warp's share of the row's loop 120), of
-// 16384 x 8 x 2048 bf16 rows with 16 entries 204 us at full clocks and 230 when the
+// 16384 x 8 x 2048 bf16 rows with 16 entries 207 us at full clocks and 233 when the
 // card has run warm (with one loop for both 264).
 #include <type_traits>
 
@@ -67,7 +67,9 @@ struct ListJoint {
 template <typename T>
 using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
 
-constexpr int kShortTop = 32;  // longest list of half a warp's row
+// Longest list of half a warp's row: two places a lane. Longer ones take a CTA a row (16384 x 8 x
+// 2048 bf16, losses and gradient: 148 and 217 us with 32 entries, 518 and 672 with 33).
+constexpr int kShortTop = 32;
 
 // Threads beside a CTA's row: its lister.
 template <int TH>

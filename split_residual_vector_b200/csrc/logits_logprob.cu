@@ -4,31 +4,32 @@
 //
 // Forward: one pass, bound by reading the row (2 or 4 bytes a logit for one
 // exponential, two sums and a maximum). Rows of up to 8 KB lie in shared memory
-// whole, half a warp each (16384 x 16 x 2048 bf16: 219 us, 4.9 TB/s; a whole warp a
+// whole, half a warp each (16384 x 16 x 2048 bf16: 221 us, 4.9 TB/s; a whole warp a
 // row spent half its instructions on what is done once a row: 247 us). A longer row
 // passes through a ring of chunks with a running maximum a warp; the ring runs on into
 // the CTA's next row while this one's sums are joined and its alternatives ordered
-// (3750 x 32000 float32: 80 us, 6.0 TB/s; with the row held in registers and 5
+// (3750 x 32000 float32: 82 us, 5.9 TB/s; with the row held in registers and 5
 // alternatives 256 us, through the ring 95 to 102).
 //
 // Alternatives: the k largest by (logit descending, id ascending). A bound that
-// at least k logits reach costs almost nothing on top of the pass: every
-// thread has its share's maximum anyway, and the k-th largest of those maxima
-// is such a bound (k threads hold a logit that reaches it). One warp finds it by
-// bisecting the values' top 16 bits; only warps with a maximum that reaches it
-// look at their logits again and append those that do to a short list, which is
-// ordered by counting. The order of appending has no influence. Where the list
-// overflows (rows of few distinct values), the bound is bisected over the keys
-// themselves, which all differ, until between k and the list's length reach it
-// (128 alternatives of 65536 x 2048 rows: 17.6 ms by k rounds of taking the next
-// largest, 1.15 so).
+// at least k logits reach comes with the pass: every thread has its share's
+// maximum anyway, and the k-th largest of those maxima is such a bound (k threads
+// hold a logit that reaches it). On long rows the list adds a fifth (82 us, so 102);
+// on short ones it is most of the work (16384 x 16 x 2048 bf16 at full clocks: 195
+// us, with 8 alternatives 451). One warp finds the bound by bisecting the values'
+// top 16 bits; only warps with a maximum that reaches it look at their logits again
+// and append those that do to a short list, which is ordered by counting. The order
+// of appending has no influence. Where the list overflows (rows of few distinct
+// values), the bound is bisected over the keys themselves, which all differ, until
+// between k and the list's length reach it (128 alternatives of 65536 x 2048 rows:
+// 17.6 ms by k rounds of taking the next largest, 1.2 so).
 //
 // Gradient: d x_i = c p_i [(z - a) - b (ln p_i + H)] + c a [i = token] from the
 // row in shared memory, so that it is read once from global memory and written
 // once. What decides whether a row is needed at all (its token and upstream
 // gradients) is loaded a row ahead of its logits. Bound by that traffic: 3750 x
 // 32000 bf16 94 to 101 us (a copy of the tensor takes 80), 3750 x 16 x 2048 float32
-// 176 (a copy 154).
+// 176 to 180 (a copy 154).
 #include "logits.cuh"
 
 namespace mimi {
